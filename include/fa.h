@@ -302,10 +302,144 @@ fa_status_t fa_bwd_dq_post(const void* workspace, size_t workspace_bytes, void* 
                            int B, int H, int N, int d, float scale, void* stream);
 
 /*
+ * Norm and position rotation of queries and keys, in front of the attention kernels (the pages
+ * have no counterpart).  For every row x of d values of head h, with the weight w of its kind and
+ * the token's position p:
+ *     r = 1 / sqrt(mean(x^2) + eps),  y = x r w,
+ *     out_a = y_a cos_i - y_b sin_i,  out_b = y_b cos_i + y_a sin_i
+ * for the rotated pairs i = 0 .. rot/2 - 1: (a, b) = (i, i + rot/2), or (2i, 2i + 1) with
+ * interleaved = 1; elements from rot on are y.  fp32 inside, one rounding to the output type.
+ *   q, k        : in,  bf16 [B, N, Hq, d] and [B, N, Hk, d] by the strides *_sb, *_sn, *_sh (in
+ *                 elements, multiples of 8) of batch, token and head; d contiguous
+ *   wq, wk      : in,  bf16 [d], or NULL for weights of 1
+ *   rope        : in,  fp32 [rope_rows, 2, rot/2]: row p holds cos, then sin, of position p's
+ *                 angles; NULL when rot == 0 (norm only)
+ *   rot         : 0 or a multiple of 16 up to d
+ *   positions   : in,  int32 [B, N] with batch stride pos_sb (0: one row for every batch), or
+ *                 NULL for position n at token n (then rope_rows >= N)
+ *   q_out, k_out: out, bf16 [B, Hq, N, d] and [B, Hk, N, d], contiguous: what fa_fwd reads
+ * Hq or Hk may be 0 (its pointers are then not looked at).  A position outside [0, rope_rows) sets
+ * the device status word (FA_ERR_DEVICE_CHECK) and leaves the token's rows as they were.  Outputs
+ * must not overlap inputs.  d in {64, 128}; pointers 16-byte aligned (positions 4); eps finite,
+ * >= 0.
+ *
+ * fa_qk_norm_rope_bwd: the gradients, from g = gradient of the outputs (gq, gk: contiguous, as
+ * q_out, k_out).  dq, dk: bf16 [B, N, H, d] by their own strides; dwq, dwk: fp32 [d], summed over
+ * all rows in a fixed order (equal calls give equal bits), or NULL.  All are overwritten; dwq and
+ * dwk are zeroed for an empty problem.  A token whose position is outside the table adds nothing.
+ *   workspace : fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d) bytes, 256-byte aligned;
+ *               contents on entry do not matter.  Concurrent calls need distinct workspaces.
+ */
+fa_status_t fa_qk_norm_rope(const void* q, const void* k, const void* wq, const void* wk, const float* rope,
+                            int rope_rows, int rot, int interleaved, const int* positions, long long pos_sb,
+                            void* q_out, void* k_out, int B, int N, int Hq, int Hk, int d,
+                            long long q_sb, long long q_sn, long long q_sh,
+                            long long k_sb, long long k_sn, long long k_sh, float eps, void* stream);
+size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int Hq, int Hk, int d);
+fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, const void* k, const void* wq,
+                                const void* wk, const float* rope, int rope_rows, int rot, int interleaved,
+                                const int* positions, long long pos_sb, void* dq, void* dk, float* dwq, float* dwk,
+                                void* workspace, size_t workspace_bytes, int B, int N, int Hq, int Hk, int d,
+                                long long q_sb, long long q_sn, long long q_sh,
+                                long long k_sb, long long k_sn, long long k_sh,
+                                long long dq_sb, long long dq_sn, long long dq_sh,
+                                long long dk_sb, long long dk_sn, long long dk_sh, float eps, void* stream);
+
+/*
+ * A paged key/value cache for serving (the pages have no counterpart): K and V live in two pools
+ * of num_pages pages of page_size tokens, [num_pages, page_size, Hk, d] by common strides c_sp,
+ * c_st, c_sh (elements) of page, token and head, d contiguous, every stride a multiple of 16
+ * bytes.  cache_fp8 = 0: bf16; 1: E4M3 codes standing for code * descale[head] (k_descale,
+ * v_descale: fp32 [Hk], or NULL for 1).  A request's tokens are at the pages that its row of the
+ * block table names: token j in page table[j / page_size], at j % page_size; slot = page *
+ * page_size + offset.  page_size and num_pages: any values >= 1 (page_size * num_pages < 2^62).
+ *
+ * fa_paged_plan: the pages and slots of one step, from the requests' lengths, on the device.
+ * Request b holds cached[b] tokens in its first ceil(cached[b] / page_size) pages; new_tokens[b]
+ * (>= 0) are added, or, for -1, the request ends and gives its pages back.
+ *   cached, new_tokens : in,  int32 [R], R <= FA_PLAN_MAX_REQUESTS
+ *   block_table        : in/out, int32 [R, table_cols], row stride table_stride; the new pages are
+ *                        entered, other entries stay
+ *   free_pages         : in/out, int32 [pool_pages]: a stack, its first free_count entries the
+ *                        free pages.  Released pages are pushed in the order (request, page);
+ *                        then wanted pages are popped from the top in the same order.
+ *   free_count         : in,  int32 [1]
+ *   lens               : out, int32 [R]: cached + new, 0 for an ended request; may be `cached`
+ *   cu_tokens          : out, int32 [R + 1]: prefix sums of the new tokens
+ *   slots, positions, token_req
+ *                      : out, int64, int32, int32 [max_tokens]: slot, position and request of every
+ *                        new token, request after request; -1, 0, -1 past the last
+ *   free_count_out     : out, int32 [1]; may be `free_count`
+ *   plan_status        : out, int32 [1]: 0, or the FA_PLAN_* reasons why the step cannot be
+ *                        planned; then nothing changes (lens = cached, free_count_out =
+ *                        free_count, cu_tokens 0, slots -1)
+ * table_cols * page_size <= FA_PAGED_MAX_LEN, max_tokens <= FA_PAGED_MAX_LEN (it may be 0).  Pointers 4-byte aligned, slots 8.
+ *
+ * fa_paged_append: the norm and rotation of fa_qk_norm_rope for T tokens, with the keys and the
+ * values written to the cache.
+ *   q, k, v   : in,  bf16 [T, Hq, d], [T, Hk, d], [T, Hk, d] by strides *_st, *_sh
+ *   wq, wk, rope, rot, interleaved, eps : as fa_qk_norm_rope (positions: int32 [T], required
+ *               when rot > 0)
+ *   slots     : in,  int64 [T]; a negative slot skips the token (its row of q_out stays as it
+ *               was).  Two tokens with one slot: which is kept is not specified.
+ *   q_out     : out, bf16 [T, Hq, d]
+ *   k_cache, v_cache : in/out.  E4M3: value / descale rounded to nearest even, saturating.
+ * A slot past the pool or a position outside the table sets the device status word and skips the
+ * token.
+ *
+ * fa_paged_decode: attention of one query token per row over the cache, split over the cache's
+ * length so that every SM has equal work whatever the lengths are, and joined with the merge of
+ * "Flash Attention" (special-jiahao.github.io, section 增量求解 softmax).
+ *   q         : in,  bf16 [T, Hq, d] by strides q_st, q_sh; head h reads kv head h / (Hq / Hk)
+ *   block_table: in, int32 [table_rows, table_cols], row stride table_stride; entries past a
+ *               row's pages are not read
+ *   lens      : in,  int32 [T]: keys that row t sees (its own included)
+ *   req       : in,  int32 [T]: row t's row of the block table, a negative one leaving the
+ *               output row as it was; NULL: row t's is t (table_rows >= T)
+ *   o, lse    : out, bf16 [T, Hq, d] and fp32 [T, Hq] (natural log); a row with lens = 0 gets
+ *               O = 0, LSE = -inf
+ *   workspace : fa_paged_decode_workspace_bytes(T, Hq, Hk, d) bytes (on the current device),
+ *               256-byte aligned; contents on entry do not matter.  Concurrent calls (two
+ *               captured graphs that may run at once, too) need distinct workspaces.
+ * Hq a multiple of Hk; table_cols * page_size <= FA_PAGED_MAX_LEN.  P is used to 16 bits (bf16 cache: a sum of two bf16 terms; E4M3 cache: one
+ * fp16 term); scores, maxima, sums and O are fp32.  A request row outside the table, a length
+ * outside [0, table_cols * page_size] or a page outside the pool sets the device status word; that
+ * row's result is then not specified, the others' are not touched by it.  A NaN reaches its own
+ * row's results; an infinite value makes its column infinite or NaN.  Equal calls give equal bits.
+ * Empty problems (T or R 0 with nothing to write, Hq + Hk 0) return FA_OK; errors as elsewhere.
+ */
+#define FA_PLAN_MAX_REQUESTS 16384
+#define FA_PAGED_MAX_LEN 2147418112 /* 2^31 - 2^16 */
+#define FA_PLAN_NO_PAGES 1
+#define FA_PLAN_ROW_FULL 2
+#define FA_PLAN_TOO_MANY_TOKENS 4
+#define FA_PLAN_BAD_INPUT 8
+fa_status_t fa_paged_plan(const int* cached, const int* new_tokens, int* block_table, long long table_stride,
+                          int table_cols, int* free_pages, int pool_pages, const int* free_count, int page_size,
+                          int R, int max_tokens, int* lens, int* cu_tokens, long long* slots, int* positions,
+                          int* token_req, int* free_count_out, int* plan_status, void* stream);
+fa_status_t fa_paged_append(const void* q, const void* k, const void* v, const void* wq, const void* wk,
+                            const float* rope, int rope_rows, int rot, int interleaved, const int* positions,
+                            const long long* slots, void* q_out, void* k_cache, void* v_cache, int cache_fp8,
+                            const float* k_descale, const float* v_descale, int num_pages, int page_size,
+                            int T, int Hq, int Hk, int d, long long q_st, long long q_sh,
+                            long long k_st, long long k_sh, long long v_st, long long v_sh,
+                            long long c_sp, long long c_st, long long c_sh, float eps, void* stream);
+size_t fa_paged_decode_workspace_bytes(int T, int Hq, int Hk, int d);
+fa_status_t fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int cache_fp8,
+                            const float* k_descale, const float* v_descale, const int* block_table,
+                            long long table_stride, int table_rows, int table_cols, const int* lens, const int* req,
+                            void* o, float* lse, void* workspace, size_t workspace_bytes,
+                            int num_pages, int page_size, int T, int Hq, int Hk, int d,
+                            long long q_st, long long q_sh, long long c_sp, long long c_st, long long c_sh,
+                            float scale, void* stream);
+
+/*
  * Synchronises `stream`, reads and clears the device status word of the current device.
  * Returns FA_ERR_TIMEOUT if a kernel's bounded wait ran out since the last call,
  * FA_ERR_DEVICE_CHECK if a device-side check failed (a full-TMEM allocation that did not start
- * at column 0, or, in the debug build, an index outside its range), FA_ERR_CUDA if the
+ * at column 0; a position, slot, length, request or page outside its range in the paged-cache and
+ * rotation calls; or, in the debug build, an index outside its range), FA_ERR_CUDA if the
  * synchronisation itself failed, FA_OK otherwise.
  */
 fa_status_t fa_get_device_status(void* stream);

@@ -137,6 +137,8 @@ int* work_counter(void* workspace, long long bh, int N, int d) {
 
 }  // namespace
 
+int device_check() { return check_device(); }
+
 // Tensor maps depend only on (address, shape, box, element type, swizzle), so encoded maps are
 // cached under that key: a map found here is exactly what encoding again would produce.
 namespace {

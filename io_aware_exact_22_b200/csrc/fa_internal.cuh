@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -123,5 +124,76 @@ cudaError_t launch_bwd_dq(int d, const CUtensorMap& tq, const CUtensorMap& tk, c
 cudaError_t launch_acc_add(float* acc, const float* x, long long elems, cudaStream_t stream);
 cudaError_t launch_bwd_post(const float* dq_acc, void* dq, long long elems, float scale,
                             cudaStream_t stream);
+
+// The current device is an sm_100 part (cached per device): FA_OK, FA_ERR_UNSUPPORTED or
+// FA_ERR_CUDA as an int.
+int device_check();
+
+// ------------------------------------------------------------------ norm + rotation (fa_norm_rope.cu)
+// Strides are in elements; rows are d contiguous elements, 16-byte aligned.
+struct NormRopeArgs {
+  uint32_t* status;
+  const __nv_bfloat16 *q, *k, *v;    // v: serving form only
+  const __nv_bfloat16 *wq, *wk;      // [d], or null for 1
+  const float* rope;                 // [rope_rows, 2, rot/2]: cosines, then sines
+  const int* positions;              // [B, N] (stride pos_sb), or null for n
+  const long long* slots;            // serving form: [N]
+  __nv_bfloat16 *q_out, *k_out;      // training form: [B,H,N,d]; serving form: q_out [N,Hq,d]
+  void *k_cache, *v_cache;           // serving form
+  const float *k_descale, *v_descale;  // E4M3 cache: [Hk], or null for 1
+  long long q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, v_sn, v_sh, pos_sb;
+  long long c_sp, c_st, c_sh;        // cache strides: page, token, head
+  int num_pages, page_size;
+  int B, N, Hq, Hk, rot, rope_rows;
+  float eps;
+  int heads_per_warp, chunks;        // set by the launcher
+};
+struct NormRopeBwdArgs {
+  uint32_t* status;
+  const __nv_bfloat16 *gq, *gk;      // [B,H,N,d]
+  const __nv_bfloat16 *q, *k, *wq, *wk;
+  const float* rope;
+  const int* positions;
+  __nv_bfloat16 *dq, *dk;
+  float* partial;                    // [blocks, 2, d]
+  long long q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, dq_sb, dq_sn, dq_sh, dk_sb, dk_sn, dk_sh, pos_sb;
+  int B, N, Hq, Hk, rot, rope_rows;
+  float eps;
+  int heads_per_warp, chunks;
+};
+// mode: 0 training form, 1 bf16 cache, 2 E4M3 cache
+cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream);
+// Blocks of the backward kernel, i.e. rows of its partial weight gradients.
+int norm_rope_bwd_blocks(long long tokens, int Hq, int Hk, int d);
+cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, float* dwq, float* dwk,
+                                 cudaStream_t stream);
+
+// ------------------------------------------------------------------ paged cache (fa_paged.cu)
+struct PlanArgs {
+  const int *cached, *new_tokens, *free_count;
+  int *table, *free_pages, *lens, *cu_tokens, *positions, *token_req, *free_count_out, *plan_status;
+  long long* slots;
+  long long table_stride;
+  int table_cols, pool_pages, page_size, R, max_tokens;
+};
+cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream);
+
+struct DecodeArgs {
+  uint32_t* status;
+  const __nv_bfloat16* q;
+  const uint8_t *k, *v;              // caches
+  const float *kd, *vd;              // E4M3: [Hk], or null for 1
+  const int *table, *lens, *req;     // req null: row t reads table row t
+  __nv_bfloat16* o;                  // [T,Hq,d]
+  float* lse;                        // [T,Hq]
+  void* workspace;
+  long long q_st, q_sh;              // elements
+  long long c_sp, c_st, c_sh;        // bytes
+  long long table_stride;
+  int table_rows, table_cols, num_pages, page_size, T, Hq, Hk;
+  float scale_log2;
+};
+size_t paged_decode_workspace(int T, int Hq, int Hk, int d);
+cudaError_t launch_paged_decode(int d, bool fp8, const DecodeArgs& a, cudaStream_t stream);
 
 }  // namespace fa

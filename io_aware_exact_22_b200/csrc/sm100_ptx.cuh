@@ -15,7 +15,8 @@ namespace fa {
 enum : uint32_t {
   FA_DEV_TIMEOUT = 1u,    // a bounded wait ran out
   FA_DEV_TMEM_BASE = 2u,  // a full-TMEM allocation did not start at column 0
-  FA_DEV_BOUNDS = 8u,     // debug build: a device-side index check failed (the access was skipped)
+  FA_DEV_BOUNDS = 8u,     // a device-side index check failed (the access was skipped): the calls that read
+                          // slots, positions or pages from device memory, and the debug build
 };
 
 // What a bounded wait needs: the CTA's abort flag (shared memory) and the device status word.

@@ -1,17 +1,21 @@
 """ctypes binding over libfa.so (C ABI in include/fa.h).
 
 Every name in ``EXPORTS`` (``fa_fwd``, ``fa_bwd``, the split-KV, FP8, deterministic,
-allocation-free and sharded-pieces entry points, the status and self-test calls) has a
-function here with the C name that only marshals arguments: torch tensors supply device
-pointers and the current CUDA stream, and every step of the attention path runs in the
-library's kernels.  ``forward``, ``forward_splitkv``, ``forward_fp8`` and ``backward``
-additionally allocate the output tensors with torch (memory plumbing only).
+allocation-free and sharded-pieces entry points, the norm + rotation and paged-cache calls, the
+status and self-test calls) has a function here with the C name that only marshals arguments:
+torch tensors supply device pointers and the current CUDA stream, and every step of the
+attention path runs in the library's kernels.  ``forward``, ``forward_splitkv``,
+``forward_fp8``, ``backward``, ``qk_norm_rope``, ``qk_norm_rope_backward``, ``paged_plan``,
+``paged_append`` and ``paged_decode`` additionally check their tensors and allocate the outputs
+that are not given with torch (memory plumbing only); the last five run on the tensors' device,
+on its current stream.
 
 Loading fails loudly (``RuntimeError``) when the shared library is missing: there is no
 fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -28,11 +32,18 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_get_device_status",
            "fa_bwd_deterministic", "fa_fwd_fp8", "fa_fwd_partial", "fa_merge_partials", "fa_fwd_carry",
            "fa_bwd_prepare", "fa_bwd_accumulate", "fa_bwd_finish", "fa_bwd_contribute", "fa_bwd_acc_add",
            "fa_bwd_main", "fa_bwd_dq_post",
+           "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_bytes",
+           "fa_paged_plan", "fa_paged_append", "fa_paged_decode", "fa_paged_decode_workspace_bytes",
            "fa_debug_build", "fa_debug_visits")
 # Size of the library's built-in scratch used by fa_bwd_noalloc (include/fa.h).
 NOALLOC_MAX_SCRATCH_BYTES = 64 << 20
+# fa_paged_plan: most requests of a step and the bits of its status (include/fa.h).
+PLAN_MAX_REQUESTS = 16384
+PAGED_MAX_LEN = 2**31 - 2**16  # most tokens of a row of the block table, and of a step
+PLAN_NO_PAGES, PLAN_ROW_FULL, PLAN_TOO_MANY_TOKENS, PLAN_BAD_INPUT = 1, 2, 4, 8
 
 _lib = None
+_NO_SWITCH = contextlib.nullcontext()
 
 
 class FAError(RuntimeError):
@@ -98,6 +109,23 @@ def lib() -> ctypes.CDLL:
         L.fa_debug_build.restype = i
         L.fa_debug_visits.argtypes = [vp, sz, i, vp]
         L.fa_debug_visits.restype = i
+        ll = ctypes.c_longlong
+        rot = [vp, i, i, i, vp]  # rope, rope_rows, rot, interleaved, positions
+        L.fa_qk_norm_rope.argtypes = [vp] * 4 + rot + [ll, vp, vp] + [i] * 5 + [ll] * 6 + [f, vp]
+        L.fa_qk_norm_rope.restype = i
+        L.fa_qk_norm_rope_bwd_workspace_bytes.argtypes = [i] * 5
+        L.fa_qk_norm_rope_bwd_workspace_bytes.restype = sz
+        L.fa_qk_norm_rope_bwd.argtypes = ([vp] * 6 + rot + [ll] + [vp] * 5 + [sz] + [i] * 5 + [ll] * 12 + [f, vp])
+        L.fa_qk_norm_rope_bwd.restype = i
+        L.fa_paged_plan.argtypes = [vp, vp, vp, ll, i, vp, i, vp, i, i, i] + [vp] * 8
+        L.fa_paged_plan.restype = i
+        L.fa_paged_append.argtypes = ([vp] * 5 + rot + [vp] * 4 + [i, vp, vp] + [i] * 6 + [ll] * 9 + [f, vp])
+        L.fa_paged_append.restype = i
+        L.fa_paged_decode.argtypes = ([vp] * 3 + [i, vp, vp, vp, ll, i, i] + [vp] * 5 + [sz] + [i] * 6 + [ll] * 5
+                                      + [f, vp])
+        L.fa_paged_decode.restype = i
+        L.fa_paged_decode_workspace_bytes.argtypes = [i] * 4
+        L.fa_paged_decode_workspace_bytes.restype = sz
         L.fa_bwd_deterministic.argtypes = L.fa_bwd.argtypes
         L.fa_bwd_deterministic.restype = i
         _lib = L
@@ -234,6 +262,60 @@ def fa_bwd_workspace_bytes(B, H, N, d) -> int:
     return lib().fa_bwd_workspace_bytes(B, H, N, d)
 
 
+def fa_qk_norm_rope(q, k, wq, wk, rope, rope_rows, rot, interleaved, positions, pos_sb, q_out, k_out, B, N, Hq, Hk,
+                    d, q_strides, k_strides, eps, stream=None) -> int:
+    """q_strides, k_strides: (batch, token, head) in elements."""
+    return lib().fa_qk_norm_rope(_ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(rope), rope_rows, rot, int(interleaved),
+                                 _ptr(positions), pos_sb, _ptr(q_out), _ptr(k_out), B, N, Hq, Hk, d, *q_strides,
+                                 *k_strides, eps, _stream(stream))
+
+
+def fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d) -> int:
+    return lib().fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d)
+
+
+def fa_qk_norm_rope_bwd(gq, gk, q, k, wq, wk, rope, rope_rows, rot, interleaved, positions, pos_sb, dq, dk, dwq, dwk,
+                        workspace, workspace_bytes, B, N, Hq, Hk, d, q_strides, k_strides, dq_strides, dk_strides, eps,
+                        stream=None) -> int:
+    return lib().fa_qk_norm_rope_bwd(_ptr(gq), _ptr(gk), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(rope), rope_rows,
+                                     rot, int(interleaved), _ptr(positions), pos_sb, _ptr(dq), _ptr(dk), _ptr(dwq),
+                                     _ptr(dwk), _ptr(workspace), int(workspace_bytes), B, N, Hq, Hk, d, *q_strides,
+                                     *k_strides, *dq_strides, *dk_strides, eps, _stream(stream))
+
+
+def fa_paged_plan(cached, new_tokens, block_table, table_stride, table_cols, free_pages, pool_pages, free_count,
+                  page_size, R, max_tokens, lens, cu_tokens, slots, positions, token_req, free_count_out, plan_status,
+                  stream=None) -> int:
+    return lib().fa_paged_plan(_ptr(cached), _ptr(new_tokens), _ptr(block_table), table_stride, table_cols,
+                               _ptr(free_pages), pool_pages, _ptr(free_count), page_size, R, max_tokens, _ptr(lens),
+                               _ptr(cu_tokens), _ptr(slots), _ptr(positions), _ptr(token_req), _ptr(free_count_out),
+                               _ptr(plan_status), _stream(stream))
+
+
+def fa_paged_append(q, k, v, wq, wk, rope, rope_rows, rot, interleaved, positions, slots, q_out, k_cache, v_cache,
+                    cache_fp8, k_descale, v_descale, num_pages, page_size, T, Hq, Hk, d, q_strides, k_strides,
+                    v_strides, cache_strides, eps, stream=None) -> int:
+    """q_strides, k_strides, v_strides: (token, head); cache_strides: (page, token, head)."""
+    return lib().fa_paged_append(_ptr(q), _ptr(k), _ptr(v), _ptr(wq), _ptr(wk), _ptr(rope), rope_rows, rot,
+                                 int(interleaved), _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_cache),
+                                 _ptr(v_cache), int(cache_fp8), _ptr(k_descale), _ptr(v_descale), num_pages, page_size,
+                                 T, Hq, Hk, d, *q_strides, *k_strides, *v_strides, *cache_strides, eps,
+                                 _stream(stream))
+
+
+def fa_paged_decode_workspace_bytes(T, Hq, Hk, d) -> int:
+    return lib().fa_paged_decode_workspace_bytes(T, Hq, Hk, d)
+
+
+def fa_paged_decode(q, k_cache, v_cache, cache_fp8, k_descale, v_descale, block_table, table_stride, table_rows,
+                    table_cols, lens, req, o, lse, workspace, workspace_bytes, num_pages, page_size, T, Hq, Hk, d,
+                    q_strides, cache_strides, scale, stream=None) -> int:
+    return lib().fa_paged_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), int(cache_fp8), _ptr(k_descale),
+                                 _ptr(v_descale), _ptr(block_table), table_stride, table_rows, table_cols, _ptr(lens),
+                                 _ptr(req), _ptr(o), _ptr(lse), _ptr(workspace), int(workspace_bytes), num_pages,
+                                 page_size, T, Hq, Hk, d, *q_strides, *cache_strides, scale, _stream(stream))
+
+
 def fa_get_device_status(stream=None) -> int:
     return lib().fa_get_device_status(_stream(stream))
 
@@ -350,3 +432,273 @@ def backward(q, k, v, o, do, lse, causal: bool, scale: float | None = None, work
     if rc:
         raise FAError(rc, fn.__name__)
     return dq, dk, dv
+
+
+# ------------------------------------------------------------------ norm + rotation, paged cache
+def rope_table(rows: int, rot: int, base: float = 10000.0, device="cuda"):
+    """fp32 [rows, 2, rot/2]: cos and sin of p * base^(-2i/rot), p the row, from 64-bit angles (a
+    plan made once, with torch)."""
+    inv = base ** (-torch.arange(0, rot, 2, device=device, dtype=torch.float64) / rot)
+    ang = torch.arange(rows, device=device, dtype=torch.float64)[:, None] * inv[None]
+    return torch.stack([ang.cos(), ang.sin()], 1).float().contiguous()
+
+
+def _want(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _rows(t, name, dims, device=None):
+    """A bf16 CUDA tensor of `dims` dimensions whose last one is contiguous."""
+    if not (t.is_cuda and t.dtype is torch.bfloat16 and t.dim() == dims and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
+        raise ValueError(f"{name} must be a CUDA bf16 tensor of {dims} dimensions, the last one contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _vec(t, name, dtype, device, numel=None, shape=None):
+    """A contiguous tensor of `dtype` on `device` with that many elements, or that shape."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
+    if (numel is not None and t.numel() != numel) or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have {numel if shape is None else tuple(shape)} elements")
+
+
+def _distinct(t, name):
+    """An output's elements must lie at addresses of their own (each stride past all that the smaller
+    ones reach)."""
+    reach = 0
+    for st, n in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+        if st <= reach:
+            raise ValueError(f"{name} must not overlap itself")
+        reach += st * (n - 1)
+
+
+def _workspace(t, nbytes, device):
+    """The caller's workspace, checked, or one allocated with torch."""
+    if t is None:
+        return torch.empty(max(nbytes, 256), device=device, dtype=torch.uint8)
+    if t.dtype is not torch.uint8 or t.device != device or not t.is_contiguous() or t.numel() < nbytes:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {device}")
+    return t
+
+
+def _strides(t):
+    """Strides in elements of all but the last dimension; a dimension of one element has none."""
+    return [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape[:-1])]
+
+
+def _current(device):
+    """Makes `device` current, if it is not."""
+    return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _run(fn, name, device, *args):
+    """Calls a C-named wrapper with `device` current, on its current stream."""
+    with _current(device):
+        rc = fn(*args)
+    if rc:
+        raise FAError(rc, name)
+
+
+def _rope_args(rope, d, device):
+    """(rope, rows, rot) of a rope_table, or of None for no rotation."""
+    if rope is None:
+        return None, 0, 0
+    if rope.dim() != 3 or rope.shape[1] != 2:
+        raise ValueError("rope must be an fp32 table [rows, 2, rot/2]")
+    _vec(rope, "rope", torch.float32, device)
+    return rope, rope.shape[0], 2 * rope.shape[2]
+
+
+def _weights(wq, wk, d, device):
+    for w, n in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _vec(w, n, torch.bfloat16, device, numel=d)
+
+
+def _qk_shape(q, k):
+    _rows(q, "q", 4)
+    _rows(k, "k", 4, q.device)
+    B, N, Hq, d = q.shape
+    if k.shape[0] != B or k.shape[1] != N or k.shape[3] != d:
+        raise ValueError("q [B,N,Hq,d] and k [B,N,Hk,d] must agree in B, N and d")
+    return B, N, Hq, k.shape[2], d
+
+
+def _positions(positions, B, N, device):
+    """(tensor or None, batch stride) of int32 positions [N] or [B,N]."""
+    if positions is None:
+        return None, 0
+    if positions.dtype is not torch.int32 or positions.device != device or positions.shape[-1:] != (N,) or not (
+            positions.dim() == 1 or (positions.dim() == 2 and positions.shape[0] == B)) or not (
+            N <= 1 or positions.stride(-1) == 1):
+        raise ValueError(f"positions must be an int32 tensor [N] or [B,N] on {device}, contiguous along N")
+    return positions, positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+
+
+def qk_norm_rope(q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                 k_out=None):
+    """Per-head RMS norm and position rotation of q [B,N,Hq,d] and k [B,N,Hk,d] (bf16, any strides
+    with the last dimension contiguous, for instance views of one fused projection), written as
+    contiguous [B,Hq,N,d] and [B,Hk,N,d], the layout that ``forward`` reads.  wq, wk: bf16 [d] or
+    None; rope: ``rope_table``'s or None for the norm alone; positions: int32 [N] or [B,N], or
+    None for 0..N-1."""
+    B, N, Hq, Hk, d = _qk_shape(q, k)
+    dev = q.device
+    _weights(wq, wk, d, dev)
+    rope, rows, rot = _rope_args(rope, d, dev)
+    positions, pos_sb = _positions(positions, B, N, dev)
+    if q_out is None:
+        q_out = torch.empty((B, Hq, N, d), device=dev, dtype=torch.bfloat16)
+    else:
+        _vec(q_out, "q_out", torch.bfloat16, dev, shape=(B, Hq, N, d))
+    if k_out is None:
+        k_out = torch.empty((B, Hk, N, d), device=dev, dtype=torch.bfloat16)
+    else:
+        _vec(k_out, "k_out", torch.bfloat16, dev, shape=(B, Hk, N, d))
+    _run(fa_qk_norm_rope, "fa_qk_norm_rope", dev, q, k, wq, wk, rope, rows, rot, interleaved, positions, pos_sb, q_out,
+         k_out, B, N, Hq, Hk, d, _strides(q), _strides(k), eps)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(gq, gk, q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interleaved: bool = False,
+                          dq=None, dk=None, workspace=None):
+    """dq, dk (bf16 [B,N,H,d]), dwq, dwk (fp32 [d]) from gq [B,Hq,N,d], gk [B,Hk,N,d], the
+    gradients of qk_norm_rope's outputs (``backward``'s dq, dk); dq, dk may be given as views, for
+    instance of a fused projection's gradient."""
+    B, N, Hq, Hk, d = _qk_shape(q, k)
+    dev = q.device
+    _vec(gq, "gq", torch.bfloat16, dev, shape=(B, Hq, N, d))
+    _vec(gk, "gk", torch.bfloat16, dev, shape=(B, Hk, N, d))
+    _weights(wq, wk, d, dev)
+    rope, rows, rot = _rope_args(rope, d, dev)
+    positions, pos_sb = _positions(positions, B, N, dev)
+    dq = torch.empty((B, N, Hq, d), device=dev, dtype=torch.bfloat16) if dq is None else dq
+    dk = torch.empty((B, N, Hk, d), device=dev, dtype=torch.bfloat16) if dk is None else dk
+    for t, n, like in ((dq, "dq", q), (dk, "dk", k)):
+        _rows(t, n, 4, dev)
+        if t.shape != like.shape:
+            raise ValueError(f"{n} must have the shape {tuple(like.shape)}")
+        _distinct(t, n)
+    dw = torch.empty((2, d), device=dev, dtype=torch.float32)
+    workspace = _workspace(workspace, fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d), dev)
+    _run(fa_qk_norm_rope_bwd, "fa_qk_norm_rope_bwd", dev, gq, gk, q, k, wq, wk, rope, rows, rot, interleaved, positions,
+         pos_sb, dq, dk, dw[0], dw[1], workspace, workspace.numel(), B, N, Hq, Hk, d, _strides(q), _strides(k),
+         _strides(dq), _strides(dk), eps)
+    return dq, dk, dw[0], dw[1]
+
+
+def paged_plan(cached, new_tokens, block_table, free_pages, free_count, page_size: int, lens, cu_tokens, slots,
+               positions, token_req, free_count_out, status):
+    """One serving step's pages and slots (fa_paged_plan): int32 CUDA tensors cached [R], new_tokens
+    [R] (-1 ends a request), block_table [R, cols] (updated), free_pages [pool] and free_count [1]
+    (the stack of free pages, updated) in; lens [R], cu_tokens [R+1], slots (int64), positions,
+    token_req [max_tokens], free_count_out [1], status [1] out.  lens may be ``cached`` and
+    free_count_out ``free_count``.  Nothing is read back: a step that cannot be planned leaves a
+    non-zero status (PLAN_*) on the device, slots of -1 and everything else as it was."""
+    dev, R, most = cached.device, cached.numel(), slots.numel()
+    _want(cached.is_cuda, "cached must be a CUDA tensor")
+    for t, n, count in ((cached, "cached", R), (new_tokens, "new_tokens", R), (free_count, "free_count", 1),
+                        (free_pages, "free_pages", None), (lens, "lens", R), (cu_tokens, "cu_tokens", R + 1),
+                        (positions, "positions", most), (token_req, "token_req", most),
+                        (free_count_out, "free_count_out", 1), (status, "status", 1)):
+        _vec(t, n, torch.int32, dev, numel=count)
+    _vec(slots, "slots", torch.int64, dev)
+    stride = _table(block_table, dev)
+    _want(block_table.shape[0] == R, "block_table must have a row for each request")
+    _run(fa_paged_plan, "fa_paged_plan", dev, cached, new_tokens, block_table, stride, block_table.shape[1], free_pages,
+         free_pages.numel(), free_count, page_size, R, most, lens, cu_tokens, slots, positions, token_req,
+         free_count_out, status)
+
+
+def _table(t, device):
+    """Row stride of a block table."""
+    if not (t.dtype is torch.int32 and t.device == device and t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1)):
+        raise ValueError(f"block_table must be an int32 tensor [rows, cols] on {device}, its rows contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _cache(k_cache, v_cache, device):
+    """(fp8, pages, page_size, Hk, d, strides) of the two pools."""
+    fp8 = k_cache.element_size() == 1
+    if (k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype is not v_cache.dtype
+            or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8)
+            or k_cache.device != device or v_cache.device != device or k_cache.stride(3) != 1):
+        raise ValueError("k_cache, v_cache must be bf16 or E4M3 tensors [pages, page_size, Hk, d] of one shape on "
+                         f"{device}, the last dimension contiguous")
+    strides = _strides(k_cache)
+    if strides != _strides(v_cache) or v_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    return (fp8, *k_cache.shape, strides)
+
+
+def _descales(k_descale, v_descale, fp8, Hk, device):
+    for t, n in ((k_descale, "k_descale"), (v_descale, "v_descale")):
+        if t is not None:
+            _want(fp8, f"{n} belongs to an E4M3 cache")
+            _vec(t, n, torch.float32, device, numel=Hk)
+
+
+def paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps: float = 1e-6,
+                 interleaved: bool = False, k_descale=None, v_descale=None, q_out=None):
+    """qk_norm_rope for T new tokens, q [T,Hq,d], k, v [T,Hk,d] (bf16, strided views allowed), with k
+    and v written to the paged cache at ``slots`` (int64 [T]; negative: the token is skipped and
+    its row of q_out stays as it was).  Returns q_out [T,Hq,d]."""
+    _rows(q, "q", 3)
+    dev = q.device
+    _rows(k, "k", 3, dev)
+    _rows(v, "v", 3, dev)
+    T, Hq, d = q.shape
+    fp8, pages, ps, Hk, dc, cst = _cache(k_cache, v_cache, dev)
+    _want(k.shape == (T, Hk, d) and v.shape == k.shape and dc == d,
+          "k and v must be [T,Hk,d] with the cache's Hk and q's T and d")
+    _weights(wq, wk, d, dev)
+    rope, rows, rot = _rope_args(rope, d, dev)
+    if positions is not None:
+        _vec(positions, "positions", torch.int32, dev, numel=T)
+    else:
+        _want(rot == 0, "positions are needed for the rotation")
+    _vec(slots, "slots", torch.int64, dev, numel=T)
+    _distinct(k_cache, "k_cache")
+    _distinct(v_cache, "v_cache")
+    _descales(k_descale, v_descale, fp8, Hk, dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), device=dev, dtype=torch.bfloat16)
+    else:
+        _vec(q_out, "q_out", torch.bfloat16, dev, shape=(T, Hq, d))
+    _run(fa_paged_append, "fa_paged_append", dev, q, k, v, wq, wk, rope, rows, rot, interleaved, positions, slots, q_out,
+         k_cache, v_cache, fp8, k_descale, v_descale, pages, ps, T, Hq, Hk, d, _strides(q), _strides(k), _strides(v),
+         cst, eps)
+    return q_out
+
+
+def paged_decode(q, k_cache, v_cache, block_table, lens, scale: float | None = None, req=None, k_descale=None,
+                 v_descale=None, out=None, lse=None, workspace=None):
+    """O [T,Hq,d] (bf16), LSE [T,Hq] of one query token per row, q [T,Hq,d], over the paged cache: row
+    t sees lens[t] keys (int32, on the device) of row req[t] of the block table (int32; None: of
+    row t; negative: the output row stays as it was).  A row with no key gets O = 0, LSE = -inf."""
+    _rows(q, "q", 3)
+    dev = q.device
+    T, Hq, d = q.shape
+    fp8, pages, ps, Hk, dc, cst = _cache(k_cache, v_cache, dev)
+    _want(dc == d and Hk > 0 and Hq % Hk == 0, "q's heads must be a multiple of the cache's, with its d")
+    stride = _table(block_table, dev)
+    _vec(lens, "lens", torch.int32, dev, numel=T)
+    if req is not None:
+        _vec(req, "req", torch.int32, dev, numel=T)
+    _descales(k_descale, v_descale, fp8, Hk, dev)
+    if out is None:
+        out = torch.empty((T, Hq, d), device=dev, dtype=torch.bfloat16)
+    else:
+        _vec(out, "out", torch.bfloat16, dev, shape=(T, Hq, d))
+    if lse is None:
+        lse = torch.empty((T, Hq), device=dev, dtype=torch.float32)
+    else:
+        _vec(lse, "lse", torch.float32, dev, shape=(T, Hq))
+    with _current(dev):
+        workspace = _workspace(workspace, fa_paged_decode_workspace_bytes(T, Hq, Hk, d), dev)
+    _run(fa_paged_decode, "fa_paged_decode", dev, q, k_cache, v_cache, fp8, k_descale, v_descale, block_table, stride,
+         block_table.shape[0], block_table.shape[1], lens, req, out, lse, workspace, workspace.numel(), pages, ps, T, Hq,
+         Hk, d, _strides(q), cst, d ** -0.5 if scale is None else scale)
+    return out, lse
