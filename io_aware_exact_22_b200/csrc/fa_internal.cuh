@@ -192,8 +192,10 @@ struct DecodeArgs {
   long long table_stride;
   int table_rows, table_cols, num_pages, page_size, T, Hq, Hk;
   float scale_log2;
+  uint64_t page_mul;                 // set by the launcher: division by page_size
+  int page_shift, hp;                // hp: kv heads that a CTA reads side by side (1, 2, 4)
 };
 size_t paged_decode_workspace(int T, int Hq, int Hk, int d);
-cudaError_t launch_paged_decode(int d, bool fp8, const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_decode(int d, bool fp8, DecodeArgs a, cudaStream_t stream);
 
 }  // namespace fa

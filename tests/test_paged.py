@@ -438,14 +438,13 @@ def test_decode_cache_layouts(cuda_ok, fp8):
     lens, ps = [50, 21], 16
     kc, vc, table = _pool(lens, ps, 4, 128, fp8, 3)
     q = torch.randn(2, 8, 128, device="cuda").bfloat16()
-    want = fa.paged_decode(q, kc, vc, _ints(table), _ints(lens))
     heads = [c.view(torch.uint8 if fp8 else torch.bfloat16).transpose(1, 2).contiguous().transpose(1, 2) for c in (kc, vc)]
     joint = torch.stack([c.view(torch.uint8 if fp8 else torch.bfloat16) for c in (kc, vc)], 1)
     wide = torch.full((2, 9), -1, dtype=torch.int32, device="cuda")
     wide[:, :len(table[0])] = _ints(table)
     for a, b, t in ((*heads, _ints(table)), (joint[:, 0], joint[:, 1], wide), (kc, vc, wide[:, :len(table[0])])):
-        got = fa.paged_decode(q, a, b, t, _ints(lens))
-        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        o, lse = fa.paged_decode(q, a, b, t, _ints(lens))
+        _check_decode(q, a, b, table, lens, range(2), o, lse, 128 ** -0.5, fp8)
     assert fa.fa_get_device_status() == OK
 
 
