@@ -146,7 +146,7 @@ struct NormRopeArgs {
   int num_pages, page_size;
   int B, N, Hq, Hk, rot, rope_rows;
   float eps;
-  int heads_per_warp, chunks;        // set by the launcher
+  int heads_per_unit, chunks;        // set by the launcher
 };
 struct NormRopeBwdArgs {
   uint32_t* status;
@@ -155,11 +155,11 @@ struct NormRopeBwdArgs {
   const float* rope;
   const int* positions;
   __nv_bfloat16 *dq, *dk;
-  float* partial;                    // [blocks, 2, d]
+  float* partial;                    // [blocks, d]
   long long q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, dq_sb, dq_sn, dq_sh, dk_sb, dk_sn, dk_sh, pos_sb;
   int B, N, Hq, Hk, rot, rope_rows;
   float eps;
-  int heads_per_warp, chunks;
+  int heads_per_unit, blocks_q;      // set by the launcher
 };
 // mode: 0 training form, 1 bf16 cache, 2 E4M3 cache
 cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream);

@@ -9,10 +9,15 @@
 //     dy = R^T g,  dw = sum over rows of dy (x r),  u = dy w,  dx = r (u - xh mean(u xh)),  xh = x r,
 // with r recomputed from x (the row is read for xh anyway, so a saved r would only add traffic).
 //
-// Layout: a lane holds 8 consecutive elements of a row (one 16-byte access), so a row is d/8
-// lanes and a warp holds 2 (d = 128) or 4 (d = 64) rows at a time.  A warp keeps one token's cos
-// and sin in registers and walks over its heads: the table row, as long as one row of data in
-// fp32, is then read once per token instead of once per head.
+// Layout: a lane holds 16 elements of a row, two 16-byte chunks that a rotation maps into each
+// other (halves: chunk j of the first half of the rotated elements and of the second), so the
+// rotation needs no exchange between lanes; a row is d/16 lanes, and a warp holds 4 (d = 128) or 8
+// (d = 64) neighbouring tokens at a time.  A lane keeps its token's cos and sin in registers and
+// walks over heads: the table row, as long as one row of data in fp32, is then read once per token
+// instead of once per head, and the stores of neighbouring tokens adjoin.
+// Rows come through a ring in shared memory that a lane fills (16-byte asynchronous copies) and
+// reads for itself: bytes in flight then cost no registers, which hold too few of them at the
+// occupancy that the arithmetic leaves, and no barrier is needed.
 #include "fa_internal.cuh"
 #include "sm100_ptx.cuh"
 
@@ -25,14 +30,17 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kDepth = 6;     // rows of the forward's ring
+constexpr int kBwdDepth = 3;  // rows of x, and of g, of the backward's
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
@@ -56,320 +64,445 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// One lane's share of a token's rotation.  Halves: element i of the first `rot` pairs with
-// i +- rot/2, which lies in another lane (`src`); the sign of the sine is folded into s.
-// Interleaved: pairs (2i, 2i+1) lie in the lane itself and use c[0..3], s[0..3].
+// One lane's share of a token's rotation: its chunks a and b (8 elements each), whether they are
+// rotated, and the angles.  Halves: pair e is (a_e, b_e) with c[e], s[e]; both chunks are rotated or
+// neither is.  Interleaved: pair i < 4 is (a_2i, a_2i+1) with c[i], s[i], and b's have c[4 + i], s[4 + i].
+template <int D, bool INTER>
 struct Rotation {
+  static constexpr int LPR = D / 16;
   float c[8], s[8];
-  int src;
-  bool on;  // the lane's elements are rotated
+  int ca, cb;
+  bool on_a, on_b;
+
+  __device__ __forceinline__ Rotation(int rot, int j) {
+    if (INTER) {
+      ca = j, cb = j + LPR;
+      on_a = 8 * ca < rot, on_b = 8 * cb < rot;
+    } else {
+      const int hl = rot >> 4;
+      on_a = on_b = j < hl;
+      ca = on_a ? j : hl + j;  // the rest of the chunks, from 2 hl on, halved among the other lanes
+      cb = on_a ? j + hl : LPR + j;
+    }
+  }
+  __device__ __forceinline__ void load(const float* __restrict__ rope, int rot, int pos) {
+    const float* row = rope + (size_t)pos * rot;
+    const int half = rot >> 1;
+    if (INTER) {
+      if (on_a) load4(0, row + 4 * ca, half);
+      if (on_b) load4(4, row + 4 * cb, half);
+    } else if (on_a) {
+      load4(0, row + 8 * ca, half);
+      load4(4, row + 8 * ca + 4, half);
+    }
+  }
+  // a, b <- R (a, b), or R^T (a, b) with BACK (the rotation by the negative angle)
+  template <bool BACK>
+  __device__ __forceinline__ void apply(float (&a)[8], float (&b)[8]) const {
+    if (INTER) {
+      if (on_a) inside<BACK>(a, 0);
+      if (on_b) inside<BACK>(b, 4);
+    } else if (on_a) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) turn<BACK>(a[e], b[e], e);
+    }
+  }
+
+ private:
+  __device__ __forceinline__ void load4(int i, const float* p, int half) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p + half));
+    c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+    s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+  }
+  template <bool BACK>
+  __device__ __forceinline__ void turn(float& a, float& b, int e) const {
+    const float x = a, y = b, sn = BACK ? -s[e] : s[e];
+    a = x * c[e] - y * sn;
+    b = y * c[e] + x * sn;
+  }
+  template <bool BACK>
+  __device__ __forceinline__ void inside(float (&x)[8], int i0) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn<BACK>(x[2 * i], x[2 * i + 1], i0 + i);
+  }
 };
 
-template <bool INTER>
-__device__ __forceinline__ void load_rotation(Rotation& t, const float* __restrict__ rope, int rot, int pos, int j) {
-  const int half = rot >> 1, hl = rot >> 4;
-  t.src = j;
-  t.on = 8 * j < rot;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) t.c[e] = 1.f, t.s[e] = 0.f;
-  if (!t.on) return;
-  const float* row = rope + (size_t)pos * rot;
-  if (INTER) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * j));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + 4 * j));
-    t.c[0] = c.x, t.c[1] = c.y, t.c[2] = c.z, t.c[3] = c.w;
-    t.s[0] = s.x, t.s[1] = s.y, t.s[2] = s.z, t.s[3] = s.w;
-  } else {
-    const bool first = j < hl;
-    const float* cp = row + 8 * (first ? j : j - hl);
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(cp)), c1 = __ldg(reinterpret_cast<const float4*>(cp + 4));
-    const float4 s0 = __ldg(reinterpret_cast<const float4*>(cp + half)),
-                 s1 = __ldg(reinterpret_cast<const float4*>(cp + half + 4));
-    const float sg = first ? -1.f : 1.f;
-    t.c[0] = c0.x, t.c[1] = c0.y, t.c[2] = c0.z, t.c[3] = c0.w;
-    t.c[4] = c1.x, t.c[5] = c1.y, t.c[6] = c1.z, t.c[7] = c1.w;
-    t.s[0] = sg * s0.x, t.s[1] = sg * s0.y, t.s[2] = sg * s0.z, t.s[3] = sg * s0.w;
-    t.s[4] = sg * s1.x, t.s[5] = sg * s1.y, t.s[6] = sg * s1.z, t.s[7] = sg * s1.w;
-    t.src = first ? j + hl : j - hl;
-  }
+// A lane's two chunks of a row, as stored.
+struct Raw {
+  uint4 a, b;
+};
+// A lane's ring: slot i holds chunk a at i * 1024 and chunk b 512 bytes behind it (a warp's lanes
+// side by side).
+__device__ __forceinline__ void copy_row(uint32_t slot, const __nv_bfloat16* p, int ca, int cb) {
+  cp_async16(slot, p + 8 * ca);
+  cp_async16(slot + 512, p + 8 * cb);
 }
-
-// y <- R y, or R^T y with BACK (the rotation by the negative angle).
-template <int LPR, bool INTER, bool BACK>
-__device__ __forceinline__ void rotate(float (&y)[8], const Rotation& t) {
-  if (INTER) {
-    if (!t.on) return;
+__device__ __forceinline__ Raw take_row(uint32_t slot) {
+  Raw r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w) : "r"(slot) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w) : "r"(slot + 512) : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_row(__nv_bfloat16* p, int ca, int cb, const uint4& a, const uint4& b) {
+  *reinterpret_cast<uint4*>(p + 8 * ca) = a;
+  *reinterpret_cast<uint4*>(p + 8 * cb) = b;
+}
+__device__ __forceinline__ Raw ld_weight(const __nv_bfloat16* w, int ca, int cb) {
+  const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+  if (!w) return {one, one};
+  return {__ldg(reinterpret_cast<const uint4*>(w) + ca), __ldg(reinterpret_cast<const uint4*>(w) + cb)};
+}
+// 1 / sqrt(mean of the row's squares + eps)
+template <int D>
+__device__ __forceinline__ float inv_rms(const float (&a)[8], const float (&b)[8], float eps) {
+  float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = y[2 * i], b = y[2 * i + 1], s = BACK ? -t.s[i] : t.s[i];
-      y[2 * i] = a * t.c[i] - b * s;
-      y[2 * i + 1] = b * t.c[i] + a * s;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float o = __shfl_sync(0xffffffffu, y[e], t.src, LPR);
-      const float v = y[e] * t.c[e] + (BACK ? -o : o) * t.s[e];
-      y[e] = t.on ? v : y[e];
-    }
-  }
+  for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+  return rsqrtf(row_sum<D / 16>(ss) * (1.f / D) + eps);
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8]) {
+  return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
 enum Mode { kTrain, kCacheBf16, kCacheE4m3 };
 
-// Forward.  One warp per (token, run of heads_per_warp heads); heads count q's, then k's, then
-// (serving) v's, which are copied unchanged.
-template <int D, bool INTER, Mode MODE, int U>
-__global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const NormRopeArgs a) {
-  constexpr int LPR = D / 8, G = 32 / LPR;
-  const int lane = threadIdx.x & 31, j = lane % LPR, grp = lane / LPR;
+// Forward.  A run of D/16 lanes per (token, run of heads_per_unit heads); heads count q's, then
+// k's, then (serving) v's, which are copied unchanged.
+template <int D, bool INTER, Mode MODE>
+__global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int LPR = D / 16, G = 32 / LPR;
+  __shared__ __align__(16) uint8_t ring[kThreads / 32 * kDepth * 1024];
+  const int lane = threadIdx.x & 31, j = lane % LPR;
   const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long tok = unit / a.chunks;
-  if (tok >= (long long)a.B * a.N) return;
-  const int h0 = (int)(unit - tok * a.chunks) * a.heads_per_warp;
+  const long long run = unit / a.chunks;
+  const long long tok = run * G + lane / LPR;
+  const int h0 = (int)(unit - run * a.chunks) * a.heads_per_unit;
   const int heads = a.Hq + a.Hk * (MODE == kTrain ? 1 : 2);
-  const int h1 = min(heads, h0 + a.heads_per_warp);
-  const int b = (int)(tok / a.N), n = (int)(tok - (long long)b * a.N);
+  const int h1 = min(heads, h0 + a.heads_per_unit);
+  const bool live = tok < (long long)a.B * a.N;
+  const int b = live ? (int)(tok / a.N) : 0, n = live ? (int)(tok - (long long)b * a.N) : 0;
+  Rotation<D, INTER> t(a.rot, j);
+
+  // What the token needs; `go`: it is computed.
+  bool go = live;
+  long long slot = 0;
+  int pos = n;
+  if (MODE != kTrain) {
+    slot = live ? a.slots[tok] : -1;
+    go = slot >= 0;
+  }
+  if (a.rot > 0 && a.positions && live) pos = a.positions[(long long)b * a.pos_sb + n];
+
+  // Rows on their way: the next head, where it is, and the last of its kind (0 q, 1 k, 2 v).
+  const uint32_t slots = smem_u32(ring) + (threadIdx.x >> 5) * (kDepth * 1024) + lane * 16;
+  auto kind_of = [&](int h) { return h < a.Hq ? 0 : MODE == kTrain || h < a.Hq + a.Hk ? 1 : 2; };
+  auto first_of = [&](int kind) { return kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + a.Hk; };
+  auto end_of = [&](int kind) { return min(h1, first_of(kind) + (kind == 0 ? a.Hq : a.Hk)); };
+  int fh = h0, fend = h0;
+  const __nv_bfloat16* fp = nullptr;
+  long long fstep = 0;
+  auto fetch = [&](int i) {
+    if (fh < h1) {
+      if (fh == fend) {
+        const int kind = kind_of(fh);
+        fend = end_of(kind);
+        fstep = kind == 0 ? a.q_sh : kind == 1 ? a.k_sh : a.v_sh;
+        fp = (kind == 0 ? a.q + b * a.q_sb + n * a.q_sn : kind == 1 ? a.k + b * a.k_sb + n * a.k_sn : a.v + n * a.v_sn) +
+             (fh - first_of(kind)) * fstep;
+      }
+      if (live) copy_row(slots + i * 1024, fp, t.ca, t.cb);
+      fp += fstep;
+      ++fh;
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) fetch(i);
 
   long long cache_off = 0;
+  bool bad = a.rot > 0 && (pos < 0 || pos >= a.rope_rows);
   if (MODE != kTrain) {
-    const long long slot = a.slots[tok];
-    if (slot < 0) return;
-    if (slot >= (long long)a.num_pages * a.page_size) {
-      if (lane == 0) atomicOr(a.status, FA_DEV_BOUNDS);
-      return;
-    }
-    const int page = (int)(slot / a.page_size);
-    cache_off = page * a.c_sp + (slot - (long long)page * a.page_size) * a.c_st;
+    bad |= slot >= (long long)a.num_pages * a.page_size;
+    const long long page = slot / a.page_size;
+    cache_off = page * a.c_sp + (slot - page * a.page_size) * a.c_st;
   }
-  Rotation t;
-  int pos = n;
-  if (a.rot > 0) {
-    if (a.positions) pos = a.positions[(long long)b * a.pos_sb + n];
-    if (pos < 0 || pos >= a.rope_rows) {
-      if (lane == 0) atomicOr(a.status, FA_DEV_BOUNDS);
-      return;
-    }
+  if (go && bad) {
+    if (j == 0) atomicOr(a.status, FA_DEV_BOUNDS);
+    go = false;
   }
-  load_rotation<INTER>(t, a.rope, a.rot, pos, j);
-  const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-  const uint4 wq = a.wq ? __ldg(reinterpret_cast<const uint4*>(a.wq) + j) : ones;
-  const uint4 wk = a.wk ? __ldg(reinterpret_cast<const uint4*>(a.wk) + j) : ones;
-  const __nv_bfloat16* qrow = a.q + b * a.q_sb + n * a.q_sn + 8 * j;
-  const __nv_bfloat16* krow = a.k + b * a.k_sb + n * a.k_sn + 8 * j;
-  const __nv_bfloat16* vrow = MODE == kTrain ? nullptr : a.v + n * a.v_sn + 8 * j;
-
-  for (int hb = h0; hb < h1; hb += U * G) {
-    uint4 x[U];
+  if (go) t.load(a.rope, a.rot, pos);
+  int slot_i = 0;
+  for (int hh = h0; hh < h1;) {
+    const int kind = kind_of(hh), end = end_of(kind);
+    int h = hh - first_of(kind);
+    float wa[8], wb[8];
+    if (MODE == kTrain || kind < 2) {
+      const Raw w = ld_weight(kind == 0 ? a.wq : a.wk, t.ca, t.cb);
+      unpack8(w.a, wa);
+      unpack8(w.b, wb);
+    }
+    // the head's row in its output, and from a head to the next, in bytes
+    char* dst;
+    long long step;
+    if (MODE == kTrain) {
+      dst = reinterpret_cast<char*>((kind == 0 ? a.q_out + (((long long)b * a.Hq + h) * a.N + n) * D
+                                               : a.k_out + (((long long)b * a.Hk + h) * a.N + n) * D));
+      step = (long long)a.N * D * 2;
+    } else if (kind == 0) {
+      dst = reinterpret_cast<char*>(a.q_out + (tok * a.Hq + h) * D), step = D * 2;
+    } else {
+      constexpr int size = MODE == kCacheBf16 ? 2 : 1;
+      dst = static_cast<char*>(kind == 2 ? a.v_cache : a.k_cache) + (cache_off + h * a.c_sh) * size, step = a.c_sh * size;
+    }
+    for (; hh < end; ++hh, ++h, dst += step) {
+      cp_wait<kDepth - 1>();
+      const Raw raw = take_row(slots + slot_i * 1024);
+      float ya[8], yb[8];
+      unpack8(raw.a, ya);
+      unpack8(raw.b, yb);
+      fetch(slot_i);
+      slot_i = slot_i == kDepth - 1 ? 0 : slot_i + 1;
+      if (MODE == kTrain || kind < 2) {
+        const float r = inv_rms<D>(ya, yb, a.eps);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * G + grp;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (h < h1) {
-        const __nv_bfloat16* p = h < a.Hq ? qrow + h * a.q_sh
-                                 : (MODE == kTrain || h < a.Hq + a.Hk) ? krow + (h - a.Hq) * a.k_sh
-                                                                       : vrow + (h - a.Hq - a.Hk) * a.v_sh;
-        x[u] = ld_stream(p);
+        for (int e = 0; e < 8; ++e) ya[e] *= r * wa[e], yb[e] *= r * wb[e];
+        t.template apply<false>(ya, yb);
       }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * G + grp;
-      float y[8], w[8];
-      unpack8(x[u], y);
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-      const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-      const bool is_q = h < a.Hq;
-      unpack8(is_q ? wq : wk, w);
-      uint4 out;
-      float z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = y[e] * r * w[e];
-      rotate<LPR, INTER, false>(z, t);
-      if (h >= h1) continue;
-      if (MODE == kTrain) {
-        out = pack8(z);
-        __nv_bfloat16* dst = is_q ? a.q_out + (((long long)b * a.Hq + h) * a.N + n) * D
-                                  : a.k_out + (((long long)b * a.Hk + (h - a.Hq)) * a.N + n) * D;
-        *reinterpret_cast<uint4*>(dst + 8 * j) = out;
-      } else if (is_q) {
-        *reinterpret_cast<uint4*>(a.q_out + (tok * a.Hq + h) * D + 8 * j) = pack8(z);
+      if (!go) continue;
+      if (MODE == kTrain || kind == 0) {
+        st_row(reinterpret_cast<__nv_bfloat16*>(dst), t.ca, t.cb, pack8(ya), pack8(yb));
+      } else if (MODE == kCacheBf16) {
+        st_row(reinterpret_cast<__nv_bfloat16*>(dst), t.ca, t.cb, kind == 2 ? raw.a : pack8(ya),
+               kind == 2 ? raw.b : pack8(yb));
       } else {
-        const bool is_v = h >= a.Hq + a.Hk;
-        const int hk = h - a.Hq - (is_v ? a.Hk : 0);
-        const long long off = cache_off + hk * a.c_sh + 8 * j;  // elements
-        if (MODE == kCacheBf16) {
-          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + off;
-          *reinterpret_cast<uint4*>(dst) = is_v ? x[u] : pack8(z);
-        } else {
-          // the value over its head's factor, rounded once to E4M3 (saturating)
-          const float* ds = is_v ? a.v_descale : a.k_descale;
-          const float f = ds ? __ldg(ds + hk) : 1.f;
+        // the value over its head's factor, rounded once to E4M3 (saturating)
+        const float* ds = kind == 2 ? a.v_descale : a.k_descale;
+        if (ds) {
+          const float f = __ldg(ds + h);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = (is_v ? y[e] : z[e]) / f;
-          uint8_t* dst = reinterpret_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + off;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_e4m3x4(z[0], z[1], z[2], z[3]),
-                                                      pack_e4m3x4(z[4], z[5], z[6], z[7]));
+          for (int e = 0; e < 8; ++e) ya[e] /= f, yb[e] /= f;
         }
+        *reinterpret_cast<uint2*>(dst + 8 * t.ca) = pack8_e4m3(ya);
+        *reinterpret_cast<uint2*>(dst + 8 * t.cb) = pack8_e4m3(yb);
       }
     }
   }
+  cp_wait<0>();
 }
 
-// Backward.  Warps walk (token, run of heads) units with a grid stride; a lane keeps the weight
-// gradients of its 8 elements in registers over all its rows, the block adds them up in shared
-// memory and writes one partial row; fa_norm_rope_dw_kernel adds the partials in block order.  No
-// atomics: equal calls give equal bits.
-template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads) fa_norm_rope_bwd_kernel(const NormRopeBwdArgs a) {
-  constexpr int LPR = D / 8, G = 32 / LPR, W = kThreads / 32;
-  __shared__ float red[W][2][D];
-  const int lane = threadIdx.x & 31, j = lane % LPR, grp = lane / LPR, warp = threadIdx.x >> 5;
-  const long long units = (long long)a.B * a.N * a.chunks;
-  const int heads = a.Hq + a.Hk;
-  const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-  const uint4 wq = a.wq ? __ldg(reinterpret_cast<const uint4*>(a.wq) + j) : ones;
-  const uint4 wk = a.wk ? __ldg(reinterpret_cast<const uint4*>(a.wk) + j) : ones;
-  float dwq[8], dwk[8];
+// Backward.  The first blocks_q blocks walk q's units, the others k's, with a grid stride; a lane
+// keeps the weight gradients of its 16 elements in registers over all its rows, the block adds
+// them up in shared memory and writes one partial row; fa_norm_rope_dw_kernel adds the partials
+// in block order.  No atomics: equal calls give equal bits.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const NormRopeBwdArgs a) {
+  constexpr int LPR = D / 16, G = 32 / LPR, W = kThreads / 32;
+  __shared__ __align__(16) uint8_t ring[W * kBwdDepth * 2048];
+  static_assert(sizeof(ring) >= W * D * 4, "the ring holds the block's sums at the end");
+  const int lane = threadIdx.x & 31, j = lane % LPR, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const bool is_q = (int)blockIdx.x < a.blocks_q;
+  const int block = is_q ? blockIdx.x : blockIdx.x - a.blocks_q;
+  const int blocks = is_q ? a.blocks_q : gridDim.x - a.blocks_q;
+  const int H = is_q ? a.Hq : a.Hk, chunks = (H + a.heads_per_unit - 1) / a.heads_per_unit;
+  const long long tokens = (long long)a.B * a.N, units = (tokens + G - 1) / G * chunks;
+  const __nv_bfloat16* const xs = is_q ? a.q : a.k;
+  const __nv_bfloat16* const gs = is_q ? a.gq : a.gk;
+  __nv_bfloat16* const dxs = is_q ? a.dq : a.dk;
+  const long long x_sh = is_q ? a.q_sh : a.k_sh, dx_sh = is_q ? a.dq_sh : a.dk_sh, g_sh = (long long)a.N * D;
+  Rotation<D, INTER> t(a.rot, j);
+  const Raw w = ld_weight(is_q ? a.wq : a.wk, t.ca, t.cb);
+  float dwa[8], dwb[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = 0.f, dwk[e] = 0.f;
+  for (int e = 0; e < 8; ++e) dwa[e] = dwb[e] = 0.f;
 
-  for (long long unit = (long long)blockIdx.x * W + warp; unit < units; unit += (long long)gridDim.x * W) {
-    const long long tok = unit / a.chunks;
-    const int h0 = (int)(unit - tok * a.chunks) * a.heads_per_warp;
-    const int h1 = min(heads, h0 + a.heads_per_warp);
-    const int b = (int)(tok / a.N), n = (int)(tok - (long long)b * a.N);
-    int pos = n;
-    if (a.rot > 0) {
-      if (a.positions) pos = a.positions[(long long)b * a.pos_sb + n];
-      if (pos < 0 || pos >= a.rope_rows) {
-        if (lane == 0) atomicOr(a.status, FA_DEV_BOUNDS);
-        continue;
+  // A place in the warp's line of units: the lane's token, a head, and where its rows are.
+  struct Place {
+    long long unit, tok;
+    const __nv_bfloat16 *x, *g;
+    int h, h1, b, n;
+  };
+  auto enter = [&](Place& p) {  // the first head of p.unit
+    const long long run = p.unit / chunks;
+    p.tok = run * G + lane / LPR;
+    p.h = (int)(p.unit - run * chunks) * a.heads_per_unit;
+    p.h1 = min(H, p.h + a.heads_per_unit);
+    if (p.tok < tokens) {
+      p.b = (int)(p.tok / a.N), p.n = (int)(p.tok - (long long)p.b * a.N);
+      p.x = xs + p.b * (is_q ? a.q_sb : a.k_sb) + p.n * (is_q ? a.q_sn : a.k_sn) + p.h * x_sh;
+      p.g = gs + (((long long)p.b * H + p.h) * a.N + p.n) * D;
+    }
+  };
+  const uint32_t slots = smem_u32(ring) + warp * (kBwdDepth * 2048) + lane * 16;
+  Place ahead;
+  ahead.unit = (long long)block * W + warp;
+  if (ahead.unit < units) enter(ahead);
+  auto fetch = [&](int i) {  // copies the rows of `ahead` and moves it on
+    if (ahead.unit < units) {
+      if (ahead.tok < tokens) {
+        copy_row(slots + i * 2048, ahead.x, t.ca, t.cb);
+        copy_row(slots + i * 2048 + 1024, ahead.g, t.ca, t.cb);
+      }
+      ahead.x += x_sh, ahead.g += g_sh;
+      if (++ahead.h == ahead.h1) {
+        ahead.unit += (long long)blocks * W;
+        if (ahead.unit < units) enter(ahead);
       }
     }
-    Rotation t;
-    load_rotation<INTER>(t, a.rope, a.rot, pos, j);
-    const __nv_bfloat16* qrow = a.q + b * a.q_sb + n * a.q_sn + 8 * j;
-    const __nv_bfloat16* krow = a.k + b * a.k_sb + n * a.k_sn + 8 * j;
-    for (int hb = h0; hb < h1; hb += U * G) {
-      uint4 x[U], g[U];
+    cp_commit();
+  };
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * G + grp;
-        x[u] = g[u] = make_uint4(0, 0, 0, 0);
-        if (h < h1) {
-          const bool is_q = h < a.Hq;
-          const int hh = is_q ? h : h - a.Hq;
-          x[u] = ld_stream(is_q ? qrow + hh * a.q_sh : krow + hh * a.k_sh);
-          const __nv_bfloat16* gp = is_q ? a.gq + (((long long)b * a.Hq + hh) * a.N + n) * D
-                                         : a.gk + (((long long)b * a.Hk + hh) * a.N + n) * D;
-          g[u] = ld_stream(gp + 8 * j);
-        }
+  for (int i = 0; i < kBwdDepth; ++i) fetch(i);
+
+  int slot_i = 0;
+  for (long long unit = (long long)block * W + warp; unit < units; unit += (long long)blocks * W) {
+    const long long run = unit / chunks;
+    const long long tok = run * G + lane / LPR;
+    const int h0 = (int)(unit - run * chunks) * a.heads_per_unit, h1 = min(H, h0 + a.heads_per_unit);
+    bool go = tok < tokens;
+    const int b = go ? (int)(tok / a.N) : 0, n = go ? (int)(tok - (long long)b * a.N) : 0;
+    int pos = n;
+    if (a.rot > 0 && a.positions && go) pos = a.positions[(long long)b * a.pos_sb + n];
+    if (go && a.rot > 0 && (pos < 0 || pos >= a.rope_rows)) {
+      if (j == 0) atomicOr(a.status, FA_DEV_BOUNDS);
+      go = false;
+    }
+    if (go) t.load(a.rope, a.rot, pos);
+    __nv_bfloat16* dst = dxs + b * (is_q ? a.dq_sb : a.dk_sb) + n * (is_q ? a.dq_sn : a.dk_sn) + h0 * dx_sh;
+    for (int h = h0; h < h1; ++h) {
+      cp_wait<kBwdDepth - 1>();
+      float xa[8], xb[8], ga[8], gb[8];
+      {
+        const Raw x = take_row(slots + slot_i * 2048), g = take_row(slots + slot_i * 2048 + 1024);
+        unpack8(x.a, xa);
+        unpack8(x.b, xb);
+        unpack8(g.a, ga);
+        unpack8(g.b, gb);
       }
+      fetch(slot_i);
+      slot_i = slot_i == kBwdDepth - 1 ? 0 : slot_i + 1;
+      t.template apply<true>(ga, gb);
+      const float r = inv_rms<D>(xa, xb, a.eps);
+      float wa[8], wb[8];
+      unpack8(w.a, wa);
+      unpack8(w.b, wb);
+      float dot = 0.f;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + u * G + grp;
-        const bool is_q = h < a.Hq;
-        float xh[8], dy[8], w[8];
-        unpack8(x[u], xh);
-        unpack8(g[u], dy);
-        rotate<LPR, INTER, true>(dy, t);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(xh[e], xh[e], ss);
-        const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-        unpack8(is_q ? wq : wk, w);
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xh[e] *= r;
-          const float p = dy[e] * xh[e];
-          if (h < h1) {
-            if (is_q) dwq[e] += p;
-            else dwk[e] += p;
-          }
-          dot = fmaf(p, w[e], dot);
-        }
-        const float c = row_sum<LPR>(dot) * (1.f / D);
-        if (h >= h1) continue;
-        float dx[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dx[e] = r * (dy[e] * w[e] - xh[e] * c);
-        __nv_bfloat16* dst = is_q ? a.dq + b * a.dq_sb + n * a.dq_sn + h * a.dq_sh
-                                  : a.dk + b * a.dk_sb + n * a.dk_sn + (h - a.Hq) * a.dk_sh;
-        *reinterpret_cast<uint4*>(dst + 8 * j) = pack8(dx);
+      for (int e = 0; e < 8; ++e) {
+        xa[e] *= r, xb[e] *= r;
+        if (go) dwa[e] = fmaf(ga[e], xa[e], dwa[e]), dwb[e] = fmaf(gb[e], xb[e], dwb[e]);
+        ga[e] *= wa[e], gb[e] *= wb[e];
+        dot = fmaf(ga[e], xa[e], fmaf(gb[e], xb[e], dot));
       }
+      const float c = row_sum<LPR>(dot) * (1.f / D);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ga[e] = r * (ga[e] - xa[e] * c);
+        gb[e] = r * (gb[e] - xb[e] * c);
+      }
+      if (go) st_row(dst, t.ca, t.cb, pack8(ga), pack8(gb));
+      dst += dx_sh;
     }
   }
+  cp_wait<0>();
+  __syncthreads();
+  float(*red)[D] = reinterpret_cast<float(*)[D]>(ring);
   // the warp's row groups, then the block's warps
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) {
-      dwq[e] += __shfl_xor_sync(0xffffffffu, dwq[e], o);
-      dwk[e] += __shfl_xor_sync(0xffffffffu, dwk[e], o);
+      dwa[e] += __shfl_xor_sync(0xffffffffu, dwa[e], o);
+      dwb[e] += __shfl_xor_sync(0xffffffffu, dwb[e], o);
     }
-    if (grp == 0) red[warp][0][8 * j + e] = dwq[e], red[warp][1][8 * j + e] = dwk[e];
+    if (lane < LPR) red[warp][8 * t.ca + e] = dwa[e], red[warp][8 * t.cb + e] = dwb[e];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kThreads) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) s += red[w][i / D][i % D];
-    a.partial[(size_t)blockIdx.x * 2 * D + i] = s;
+    for (int v = 0; v < W; ++v) s += red[v][i];
+    a.partial[(size_t)blockIdx.x * D + i] = s;
   }
 }
 
-// dw[i] = sum over blocks of partial[block][i], 32 columns per block, in a fixed order.
-__global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* __restrict__ partial, int blocks, int d,
+// dw[i] = sum over the blocks of its kind of partial[block][i], 32 columns per block, in a fixed
+// order: blockIdx.x is the columns, blockIdx.y 0 for q, 1 for k.
+__global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* partial, int blocks_q, int blocks, int d,
                                                                float* dwq, float* dwk) {
   __shared__ float red[32][33];
   const int c = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  float* const out = blockIdx.y == 0 ? dwq : dwk;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!out) return;
   float s = 0.f;
-  for (int r = y; r < blocks; r += 32) s += partial[(size_t)r * 2 * d + col];
+#pragma unroll 8
+  for (int r = (blockIdx.y == 0 ? 0 : blocks_q) + y; r < (blockIdx.y == 0 ? blocks_q : blocks); r += 32)
+    s += partial[(size_t)r * d + col];
   red[y][c] = s;
   __syncthreads();
   float v = red[c][y];  // warp y now holds column y's 32 sums
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (c == 0) {
-    const int i = blockIdx.x * 32 + y;
-    float* out = i < d ? dwq : dwk;
-    if (out) out[i < d ? i : i - d] = v;
-  }
+  if (c == 0) out[blockIdx.x * 32 + y] = v;
 }
 
-// Heads per warp: all of a token's heads when there are tokens enough to fill the GPU with a warp
-// each, else runs short enough that the warps do, in whole steps of the inner loop.
-int heads_per_warp(long long tokens, int heads, int step) {
-  const long long want = 148LL * 32;
-  long long chunks = std::max(1LL, want / std::max(1LL, tokens));
-  long long per = (heads + chunks - 1) / chunks;
-  per = (per + step - 1) / step * step;
-  return (int)per;
+// Heads per run of lanes.  With few waves of warps, the number of waves counts (a wave of `per` heads
+// costs about per + kStart heads: slots, positions and table rows arrive one after the other);
+// with many, kMaxHeads at most lets the blocks even out over the SMs: at 16384 tokens of 64 heads
+// 16 take 88 us, 32 take 94 and 8 take 97; at 4192 tokens of 40 heads, where 10 are 1.8 waves, 20
+// are one.
+constexpr int kMaxHeads = 16, kStart = 6, kWarpSlots = 148 * 16;
+int heads_per_unit(long long token_runs, int heads) {
+  const int most = std::min(heads, kMaxHeads);
+  const long long units = token_runs * ((heads + most - 1) / most);
+  if (units >= 4 * kWarpSlots) return most;
+  int best = most;
+  long long cost = (units + kWarpSlots - 1) / kWarpSlots * (most + kStart);
+  for (int waves = 1; waves <= 4; ++waves) {
+    const long long chunks = std::min<long long>(heads, (long long)waves * kWarpSlots / token_runs);
+    if (chunks < 1) continue;
+    const int per = (int)((heads + chunks - 1) / chunks);
+    const long long n = token_runs * ((heads + per - 1) / per);
+    const long long c = (n + kWarpSlots - 1) / kWarpSlots * (per + kStart);
+    if (c < cost) cost = c, best = per;
+  }
+  return best;
+}
+
+long long token_runs(long long tokens, int d) { return (tokens + 32 / (d / 16) - 1) / (32 / (d / 16)); }
+
+// Blocks of the backward kernel: four per SM, shared out by heads, and no more than there are units.
+struct BwdBlocks {
+  int per, q, k;
+};
+BwdBlocks bwd_blocks(long long tokens, int Hq, int Hk, int d) {
+  BwdBlocks r;
+  const long long runs = token_runs(tokens, d);
+  r.per = heads_per_unit(runs, Hq + Hk);
+  constexpr int all = 148 * 4, W = kThreads / 32;
+  auto need = [&](int H) { return (runs * ((H + r.per - 1) / r.per) + W - 1) / W; };
+  const int share = Hq + Hk > 0 ? (int)(((long long)all * Hq + (Hq + Hk) / 2) / (Hq + Hk)) : 0;
+  r.q = Hq == 0 ? 0 : (int)std::min<long long>(std::min(std::max(share, 1), Hk ? all - 1 : all), need(Hq));
+  r.k = Hk == 0 ? 0 : (int)std::min<long long>(std::max(all - share, 1), need(Hk));
+  return r;
 }
 
 }  // namespace
 
 int norm_rope_bwd_blocks(long long tokens, int Hq, int Hk, int d) {
-  const int G = 32 / (d / 8), U = 2;
-  const int per = heads_per_warp(tokens, Hq + Hk, U * G);
-  const long long units = tokens * ((Hq + Hk + per - 1) / per);
-  return (int)std::max(1LL, std::min(148LL * 4, (units + 7) / 8));
+  const BwdBlocks r = bwd_blocks(tokens, Hq, Hk, d);
+  return r.q + r.k;
 }
 
 cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream) {
-  constexpr int U = 4;
-  const int G = 32 / (d / 8);
   const int heads = a.Hq + a.Hk * (mode == kTrain ? 1 : 2);
-  const long long tokens = (long long)a.B * a.N;
-  a.heads_per_warp = heads_per_warp(tokens, heads, G);
-  a.chunks = (heads + a.heads_per_warp - 1) / a.heads_per_warp;
-  const long long blocks = (tokens * a.chunks + kThreads / 32 - 1) / (kThreads / 32);
+  const long long runs = token_runs((long long)a.B * a.N, d);
+  a.heads_per_unit = heads_per_unit(runs, heads);
+  a.chunks = (heads + a.heads_per_unit - 1) / a.heads_per_unit;
+  const long long blocks = (runs * a.chunks + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
-#define FA_NR(DD, II, MM) fa_norm_rope_kernel<DD, II, MM, U><<<(unsigned)blocks, kThreads, 0, stream>>>(a)
+#define FA_NR(DD, II, MM) fa_norm_rope_kernel<DD, II, MM><<<(unsigned)blocks, kThreads, 0, stream>>>(a)
 #define FA_NR_M(DD, II)                                        \
   do {                                                         \
     if (mode == kTrain) FA_NR(DD, II, kTrain);                 \
@@ -390,13 +523,10 @@ cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, 
 
 cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, float* dwq, float* dwk,
                                  cudaStream_t stream) {
-  constexpr int U = 2;
-  const int G = 32 / (d / 8);
-  const long long tokens = (long long)a.B * a.N;
-  a.heads_per_warp = heads_per_warp(tokens, a.Hq + a.Hk, U * G);
-  a.chunks = (a.Hq + a.Hk + a.heads_per_warp - 1) / a.heads_per_warp;
-  const int blocks = norm_rope_bwd_blocks(tokens, a.Hq, a.Hk, d);
-#define FA_NRB(DD, II) fa_norm_rope_bwd_kernel<DD, II, U><<<blocks, kThreads, 0, stream>>>(a)
+  const BwdBlocks r = bwd_blocks((long long)a.B * a.N, a.Hq, a.Hk, d);
+  a.heads_per_unit = r.per, a.blocks_q = r.q;
+  const int blocks = r.q + r.k;
+#define FA_NRB(DD, II) fa_norm_rope_bwd_kernel<DD, II><<<blocks, kThreads, 0, stream>>>(a)
   if (d == 64) {
     if (interleaved) FA_NRB(64, true);
     else FA_NRB(64, false);
@@ -407,8 +537,16 @@ cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, flo
 #undef FA_NRB
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (!dwq && !dwk)) return e;
-  fa_norm_rope_dw_kernel<<<2 * d / 32, 1024, 0, stream>>>(a.partial, blocks, d, dwq, dwk);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(d / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};  // its blocks may be in place before the partials are
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_norm_rope_dw_kernel, (const float*)a.partial, r.q, blocks, d, dwq, dwk);
 }
 
 }  // namespace fa

@@ -87,7 +87,7 @@ fa_status_t fa_qk_norm_rope(const void* q, const void* k, const void* wq, const 
 
 size_t fa_qk_norm_rope_bwd_workspace_bytes(int B, int N, int Hq, int Hk, int d) {
   if (!sizes_ok(B, N, Hq, Hk, d) || (d != 64 && d != 128) || (long long)B * N == 0 || Hq + Hk == 0) return 0;
-  return (size_t)norm_rope_bwd_blocks((long long)B * N, Hq, Hk, d) * 2 * d * 4;
+  return (size_t)norm_rope_bwd_blocks((long long)B * N, Hq, Hk, d) * d * 4;
 }
 
 fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, const void* k, const void* wq,
