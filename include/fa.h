@@ -311,6 +311,7 @@ fa_status_t fa_bwd_dq_post(const void* workspace, size_t workspace_bytes, void* 
  * interleaved = 1; elements from rot on are y.  fp32 inside, one rounding to the output type.
  *   q, k        : in,  bf16 [B, N, Hq, d] and [B, N, Hk, d] by the strides *_sb, *_sn, *_sh (in
  *                 elements, multiples of 8) of batch, token and head; d contiguous
+ *                 (here and below the stride of a dimension of one element is not looked at)
  *   wq, wk      : in,  bf16 [d], or NULL for weights of 1
  *   rope        : in,  fp32 [rope_rows, 2, rot/2]: row p holds cos, then sin, of position p's
  *                 angles; NULL when rot == 0 (norm only)

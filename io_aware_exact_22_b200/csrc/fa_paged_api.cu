@@ -15,11 +15,11 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // A tensor that must be there (16-byte aligned) when `used`.
 bool rows_ok(const void* p, bool used) { return !used || (p && aligned(p, 16)); }
 
-// Strides of rows handed to 16-byte accesses: multiples of `unit` elements, and small enough that
-// no offset in use overflows (|stride| * count < 2^62).
+// A stride of `count` rows handed to 16-byte accesses: a multiple of `unit` elements, and small enough
+// that no offset in use overflows (|stride| * count < 2^59).  Of one row, the stride is not looked at.
 bool stride_ok(long long s, long long count, long long unit) {
-  if (s % unit != 0) return false;
-  return std::fabs((double)s) * (double)(count > 0 ? count : 1) < 4.6e18;
+  if (count <= 1) return true;
+  return s % unit == 0 && std::fabs((double)s) * (double)count < 5.7e17;
 }
 
 // What the three norm + rotation calls share.
@@ -51,8 +51,7 @@ bool cache_ok(const void* k, const void* v, int num_pages, int page_size, int Hk
               long long c_sh, int size) {
   if (!rows_ok(k, true) || !rows_ok(v, true) || num_pages < 1 || page_size < 1) return false;
   const long long unit = 16 / size;
-  return stride_ok(c_sp, (long long)num_pages * 8, unit) && stride_ok(c_st, (long long)page_size * 8, unit) &&
-         stride_ok(c_sh, (long long)Hk * 8, unit);
+  return stride_ok(c_sp, num_pages, unit) && stride_ok(c_st, page_size, unit) && stride_ok(c_sh, Hk, unit);
 }
 
 }  // namespace
@@ -152,7 +151,7 @@ fa_status_t fa_paged_plan(const int* cached, const int* new_tokens, int* block_t
   for (const void* p : ints)
     if (!aligned(p, 4)) return FA_ERR_INVALID_ARG;
   if (!aligned(slots, 8)) return FA_ERR_INVALID_ARG;
-  if (!stride_ok(table_stride, (long long)R * 4, 1)) return FA_ERR_INVALID_ARG;
+  if (!stride_ok(table_stride, R, 1)) return FA_ERR_INVALID_ARG;
   fa_status_t st = (fa_status_t)device_check();
   if (st != FA_OK) return st;
   PlanArgs a = {};
@@ -228,7 +227,7 @@ fa_status_t fa_paged_decode(const void* q, const void* k_cache, const void* v_ca
     return FA_ERR_INVALID_ARG;
   if (!stride_ok(q_st, T, 8) || !stride_ok(q_sh, Hq, 8)) return FA_ERR_INVALID_ARG;
   if ((table_cols > 0 && table_rows > 0 && !block_table) || !aligned(block_table, 4) || table_stride < table_cols ||
-      !stride_ok(table_stride, (long long)table_rows * 4, 1) || (long long)table_cols * page_size > FA_PAGED_MAX_LEN)
+      !stride_ok(table_stride, table_rows, 1) || (long long)table_cols * page_size > FA_PAGED_MAX_LEN)
     return FA_ERR_INVALID_ARG;
   if (!req && table_rows < T) return FA_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < fa_paged_decode_workspace_bytes(T, Hq, Hk, d))

@@ -15,7 +15,6 @@ fallback implementation.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -43,7 +42,6 @@ PAGED_MAX_LEN = 2**31 - 2**16  # most tokens of a row of the block table, and of
 PLAN_NO_PAGES, PLAN_ROW_FULL, PLAN_TOO_MANY_TOKENS, PLAN_BAD_INPUT = 1, 2, 4, 8
 
 _lib = None
-_NO_SWITCH = contextlib.nullcontext()
 
 
 class FAError(RuntimeError):
@@ -443,30 +441,67 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, device="cuda"):
     return torch.stack([ang.cos(), ang.sin()], 1).float().contiguous()
 
 
-def _want(cond, what):
-    if not cond:
-        raise ValueError(what)
+# The calls below are short enough on the device for the host to be what a caller waits for, so
+# their checks read each tensor's metadata once, and they hand the C functions addresses
+# themselves.  Strides go as they are: the library does not look at the stride of a dimension of
+# one element.
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _rows(t, name, dims, device=None):
-    """A bf16 CUDA tensor of `dims` dimensions whose last one is contiguous."""
-    if not (t.is_cuda and t.dtype is torch.bfloat16 and t.dim() == dims and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
-        raise ValueError(f"{name} must be a CUDA bf16 tensor of {dims} dimensions, the last one contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+def _new(shape, dtype, device):
+    """torch.empty (contiguous) by the shorter way."""
+    strides, n = [], 1
+    for size in reversed(shape):
+        strides.append(n)
+        n *= max(size, 1)
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
 
 
-def _vec(t, name, dtype, device, numel=None, shape=None):
-    """A contiguous tensor of `dtype` on `device` with that many elements, or that shape."""
-    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device}")
-    if (numel is not None and t.numel() != numel) or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have {numel if shape is None else tuple(shape)} elements")
+def _call(name, index, *args):
+    """Calls a C function with device `index` current, on its current stream."""
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc:
+        raise FAError(rc, name)
+
+
+def _rows(t, name, dims, index):
+    """Shape of a bf16 tensor of `dims` dimensions on CUDA device `index` (any, if None), the last
+    one contiguous."""
+    shape = t.shape
+    if not (t.dtype is _BF16 and len(shape) == dims and t.is_cuda and (index is None or t.get_device() == index)
+            and (t.stride(-1) == 1 or shape[-1] <= 1)):
+        raise ValueError(f"{name} must be a bf16 tensor of {dims} dimensions, the last one contiguous, on one CUDA device")
+    return shape
+
+
+def _vec(t, name, dtype, index, numel):
+    """Address of a contiguous tensor of `dtype` and that many elements on CUDA device `index`."""
+    if not (t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.numel() == numel):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on CUDA device {index}")
+    return t.data_ptr()
+
+
+def _out(t, name, dtype, device, index, shape):
+    """An output: the caller's contiguous tensor, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, device)
+    if not (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on CUDA device {index}")
+    return t
 
 
 def _distinct(t, name):
     """An output's elements must lie at addresses of their own (each stride past all that the smaller
     ones reach)."""
+    if t.is_contiguous():
+        return
     reach = 0
     for st, n in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
         if st <= reach:
@@ -474,67 +509,47 @@ def _distinct(t, name):
         reach += st * (n - 1)
 
 
-def _workspace(t, nbytes, device):
-    """The caller's workspace, checked, or one allocated with torch."""
+def _workspace(t, nbytes, device, index):
+    """The caller's workspace, checked, or a new one."""
     if t is None:
-        return torch.empty(max(nbytes, 256), device=device, dtype=torch.uint8)
-    if t.dtype is not torch.uint8 or t.device != device or not t.is_contiguous() or t.numel() < nbytes:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on {device}")
+        return _new((max(nbytes, 256),), _U8, device)
+    if t.dtype is not _U8 or t.get_device() != index or not t.is_contiguous() or t.numel() < nbytes:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on CUDA device {index}")
     return t
 
 
-def _strides(t):
-    """Strides in elements of all but the last dimension; a dimension of one element has none."""
-    return [st if n > 1 else 0 for st, n in zip(t.stride()[:-1], t.shape[:-1])]
+def _weight(w, name, d, index):
+    return None if w is None else _vec(w, name, _BF16, index, d)
 
 
-def _current(device):
-    """Makes `device` current, if it is not."""
-    return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _run(fn, name, device, *args):
-    """Calls a C-named wrapper with `device` current, on its current stream."""
-    with _current(device):
-        rc = fn(*args)
-    if rc:
-        raise FAError(rc, name)
-
-
-def _rope_args(rope, d, device):
-    """(rope, rows, rot) of a rope_table, or of None for no rotation."""
+def _rope(rope, index):
+    """(address, rows, rot) of a rope_table, or of None for no rotation."""
     if rope is None:
         return None, 0, 0
-    if rope.dim() != 3 or rope.shape[1] != 2:
-        raise ValueError("rope must be an fp32 table [rows, 2, rot/2]")
-    _vec(rope, "rope", torch.float32, device)
-    return rope, rope.shape[0], 2 * rope.shape[2]
+    shape = rope.shape
+    if not (len(shape) == 3 and shape[1] == 2 and rope.dtype is _F32 and rope.get_device() == index
+            and rope.is_contiguous()):
+        raise ValueError(f"rope must be a contiguous fp32 table [rows, 2, rot/2] on CUDA device {index}")
+    return rope.data_ptr(), shape[0], 2 * shape[2]
 
 
-def _weights(wq, wk, d, device):
-    for w, n in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _vec(w, n, torch.bfloat16, device, numel=d)
-
-
-def _qk_shape(q, k):
-    _rows(q, "q", 4)
-    _rows(k, "k", 4, q.device)
-    B, N, Hq, d = q.shape
-    if k.shape[0] != B or k.shape[1] != N or k.shape[3] != d:
-        raise ValueError("q [B,N,Hq,d] and k [B,N,Hk,d] must agree in B, N and d")
-    return B, N, Hq, k.shape[2], d
-
-
-def _positions(positions, B, N, device):
-    """(tensor or None, batch stride) of int32 positions [N] or [B,N]."""
+def _positions(positions, B, N, index):
+    """(address or None, batch stride) of int32 positions [N] or [B,N]."""
     if positions is None:
         return None, 0
-    if positions.dtype is not torch.int32 or positions.device != device or positions.shape[-1:] != (N,) or not (
-            positions.dim() == 1 or (positions.dim() == 2 and positions.shape[0] == B)) or not (
-            N <= 1 or positions.stride(-1) == 1):
-        raise ValueError(f"positions must be an int32 tensor [N] or [B,N] on {device}, contiguous along N")
-    return positions, positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    shape = positions.shape
+    if not (positions.dtype is _I32 and positions.get_device() == index and (shape == (N,) or shape == (B, N))
+            and (N <= 1 or positions.stride(-1) == 1)):
+        raise ValueError(f"positions must be an int32 tensor [N] or [B,N], contiguous along N, on CUDA device {index}")
+    return positions.data_ptr(), positions.stride(0) if len(shape) == 2 else 0
+
+
+def _qk(q, k):
+    B, N, Hq, d = _rows(q, "q", 4, None)
+    index = q.get_device()
+    if _rows(k, "k", 4, index) != (B, N, k.shape[2], d):
+        raise ValueError("q [B,N,Hq,d] and k [B,N,Hk,d] must agree in B, N and d")
+    return B, N, Hq, k.shape[2], d, q.device, index
 
 
 def qk_norm_rope(q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
@@ -544,21 +559,14 @@ def qk_norm_rope(q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interlea
     contiguous [B,Hq,N,d] and [B,Hk,N,d], the layout that ``forward`` reads.  wq, wk: bf16 [d] or
     None; rope: ``rope_table``'s or None for the norm alone; positions: int32 [N] or [B,N], or
     None for 0..N-1."""
-    B, N, Hq, Hk, d = _qk_shape(q, k)
-    dev = q.device
-    _weights(wq, wk, d, dev)
-    rope, rows, rot = _rope_args(rope, d, dev)
-    positions, pos_sb = _positions(positions, B, N, dev)
-    if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), device=dev, dtype=torch.bfloat16)
-    else:
-        _vec(q_out, "q_out", torch.bfloat16, dev, shape=(B, Hq, N, d))
-    if k_out is None:
-        k_out = torch.empty((B, Hk, N, d), device=dev, dtype=torch.bfloat16)
-    else:
-        _vec(k_out, "k_out", torch.bfloat16, dev, shape=(B, Hk, N, d))
-    _run(fa_qk_norm_rope, "fa_qk_norm_rope", dev, q, k, wq, wk, rope, rows, rot, interleaved, positions, pos_sb, q_out,
-         k_out, B, N, Hq, Hk, d, _strides(q), _strides(k), eps)
+    B, N, Hq, Hk, d, dev, index = _qk(q, k)
+    table, rows, rot = _rope(rope, index)
+    pos, pos_sb = _positions(positions, B, N, index)
+    q_out = _out(q_out, "q_out", _BF16, dev, index, (B, Hq, N, d))
+    k_out = _out(k_out, "k_out", _BF16, dev, index, (B, Hk, N, d))
+    _call("fa_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), _weight(wq, "wq", d, index),
+          _weight(wk, "wk", d, index), table, rows, rot, interleaved, pos, pos_sb, q_out.data_ptr(), k_out.data_ptr(),
+          B, N, Hq, Hk, d, *q.stride()[:3], *k.stride()[:3], eps)
     return q_out, k_out
 
 
@@ -567,26 +575,39 @@ def qk_norm_rope_backward(gq, gk, q, k, wq, wk, rope, positions=None, eps: float
     """dq, dk (bf16 [B,N,H,d]), dwq, dwk (fp32 [d]) from gq [B,Hq,N,d], gk [B,Hk,N,d], the
     gradients of qk_norm_rope's outputs (``backward``'s dq, dk); dq, dk may be given as views, for
     instance of a fused projection's gradient."""
-    B, N, Hq, Hk, d = _qk_shape(q, k)
-    dev = q.device
-    _vec(gq, "gq", torch.bfloat16, dev, shape=(B, Hq, N, d))
-    _vec(gk, "gk", torch.bfloat16, dev, shape=(B, Hk, N, d))
-    _weights(wq, wk, d, dev)
-    rope, rows, rot = _rope_args(rope, d, dev)
-    positions, pos_sb = _positions(positions, B, N, dev)
-    dq = torch.empty((B, N, Hq, d), device=dev, dtype=torch.bfloat16) if dq is None else dq
-    dk = torch.empty((B, N, Hk, d), device=dev, dtype=torch.bfloat16) if dk is None else dk
-    for t, n, like in ((dq, "dq", q), (dk, "dk", k)):
-        _rows(t, n, 4, dev)
-        if t.shape != like.shape:
-            raise ValueError(f"{n} must have the shape {tuple(like.shape)}")
-        _distinct(t, n)
-    dw = torch.empty((2, d), device=dev, dtype=torch.float32)
-    workspace = _workspace(workspace, fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d), dev)
-    _run(fa_qk_norm_rope_bwd, "fa_qk_norm_rope_bwd", dev, gq, gk, q, k, wq, wk, rope, rows, rot, interleaved, positions,
-         pos_sb, dq, dk, dw[0], dw[1], workspace, workspace.numel(), B, N, Hq, Hk, d, _strides(q), _strides(k),
-         _strides(dq), _strides(dk), eps)
-    return dq, dk, dw[0], dw[1]
+    B, N, Hq, Hk, d, dev, index = _qk(q, k)
+    if gq.shape != (B, Hq, N, d) or gk.shape != (B, Hk, N, d):
+        raise ValueError("gq and gk must be [B,Hq,N,d] and [B,Hk,N,d]")
+    table, rows, rot = _rope(rope, index)
+    pos, pos_sb = _positions(positions, B, N, index)
+    if dq is None:
+        dq = _new((B, N, Hq, d), _BF16, dev)
+    elif _rows(dq, "dq", 4, index) != q.shape:
+        raise ValueError(f"dq must have the shape {tuple(q.shape)}")
+    else:
+        _distinct(dq, "dq")
+    if dk is None:
+        dk = _new((B, N, Hk, d), _BF16, dev)
+    elif _rows(dk, "dk", 4, index) != k.shape:
+        raise ValueError(f"dk must have the shape {tuple(k.shape)}")
+    else:
+        _distinct(dk, "dk")
+    dwq, dwk = _new((d,), _F32, dev), _new((d,), _F32, dev)
+    workspace = _workspace(workspace, fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d), dev, index)
+    _call("fa_qk_norm_rope_bwd", index, _vec(gq, "gq", _BF16, index, B * Hq * N * d),
+          _vec(gk, "gk", _BF16, index, B * Hk * N * d), q.data_ptr(), k.data_ptr(), _weight(wq, "wq", d, index),
+          _weight(wk, "wk", d, index), table, rows, rot, interleaved, pos, pos_sb, dq.data_ptr(), dk.data_ptr(),
+          dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(), B, N, Hq, Hk, d, *q.stride()[:3],
+          *k.stride()[:3], *dq.stride()[:3], *dk.stride()[:3], eps)
+    return dq, dk, dwq, dwk
+
+
+def _table(t, index):
+    """(address, row stride, rows, columns) of a block table."""
+    shape = t.shape
+    if not (t.dtype is _I32 and t.get_device() == index and len(shape) == 2 and (shape[1] <= 1 or t.stride(1) == 1)):
+        raise ValueError(f"block_table must be an int32 tensor [rows, cols], its rows contiguous, on CUDA device {index}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1], *shape
 
 
 def paged_plan(cached, new_tokens, block_table, free_pages, free_count, page_size: int, lens, cu_tokens, slots,
@@ -597,47 +618,39 @@ def paged_plan(cached, new_tokens, block_table, free_pages, free_count, page_siz
     token_req [max_tokens], free_count_out [1], status [1] out.  lens may be ``cached`` and
     free_count_out ``free_count``.  Nothing is read back: a step that cannot be planned leaves a
     non-zero status (PLAN_*) on the device, slots of -1 and everything else as it was."""
-    dev, R, most = cached.device, cached.numel(), slots.numel()
-    _want(cached.is_cuda, "cached must be a CUDA tensor")
-    for t, n, count in ((cached, "cached", R), (new_tokens, "new_tokens", R), (free_count, "free_count", 1),
-                        (free_pages, "free_pages", None), (lens, "lens", R), (cu_tokens, "cu_tokens", R + 1),
-                        (positions, "positions", most), (token_req, "token_req", most),
-                        (free_count_out, "free_count_out", 1), (status, "status", 1)):
-        _vec(t, n, torch.int32, dev, numel=count)
-    _vec(slots, "slots", torch.int64, dev)
-    stride = _table(block_table, dev)
-    _want(block_table.shape[0] == R, "block_table must have a row for each request")
-    _run(fa_paged_plan, "fa_paged_plan", dev, cached, new_tokens, block_table, stride, block_table.shape[1], free_pages,
-         free_pages.numel(), free_count, page_size, R, most, lens, cu_tokens, slots, positions, token_req,
-         free_count_out, status)
+    if not cached.is_cuda:
+        raise ValueError("cached must be a CUDA tensor")
+    index, R, most, pool = cached.get_device(), cached.numel(), slots.numel(), free_pages.numel()
+    table, stride, rows, cols = _table(block_table, index)
+    if rows != R:
+        raise ValueError("block_table must have a row for each request")
+    _call("fa_paged_plan", index, _vec(cached, "cached", _I32, index, R), _vec(new_tokens, "new_tokens", _I32, index, R),
+          table, stride, cols, _vec(free_pages, "free_pages", _I32, index, pool), pool,
+          _vec(free_count, "free_count", _I32, index, 1), page_size, R, most, _vec(lens, "lens", _I32, index, R),
+          _vec(cu_tokens, "cu_tokens", _I32, index, R + 1), _vec(slots, "slots", _I64, index, most),
+          _vec(positions, "positions", _I32, index, most), _vec(token_req, "token_req", _I32, index, most),
+          _vec(free_count_out, "free_count_out", _I32, index, 1), _vec(status, "status", _I32, index, 1))
 
 
-def _table(t, device):
-    """Row stride of a block table."""
-    if not (t.dtype is torch.int32 and t.device == device and t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1)):
-        raise ValueError(f"block_table must be an int32 tensor [rows, cols] on {device}, its rows contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _cache(k_cache, v_cache, device):
-    """(fp8, pages, page_size, Hk, d, strides) of the two pools."""
-    fp8 = k_cache.element_size() == 1
-    if (k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype is not v_cache.dtype
-            or k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8)
-            or k_cache.device != device or v_cache.device != device or k_cache.stride(3) != 1):
-        raise ValueError("k_cache, v_cache must be bf16 or E4M3 tensors [pages, page_size, Hk, d] of one shape on "
-                         f"{device}, the last dimension contiguous")
-    strides = _strides(k_cache)
-    if strides != _strides(v_cache) or v_cache.stride(3) != 1:
+def _cache(k_cache, v_cache, index):
+    """(fp8, shape, strides) of the two pools."""
+    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if not (len(shape) == 4 and v_cache.shape == shape and v_cache.dtype is dtype
+            and (dtype is _BF16 or dtype is torch.float8_e4m3fn or dtype is _U8) and strides[3] == 1
+            and k_cache.get_device() == index and v_cache.get_device() == index):
+        raise ValueError("k_cache, v_cache must be bf16 or E4M3 tensors [pages, page_size, Hk, d] of one shape, the last "
+                         f"dimension contiguous, on CUDA device {index}")
+    if v_cache.stride() != strides:
         raise ValueError("k_cache and v_cache must have the same strides")
-    return (fp8, *k_cache.shape, strides)
+    return dtype is not _BF16, shape, strides
 
 
-def _descales(k_descale, v_descale, fp8, Hk, device):
-    for t, n in ((k_descale, "k_descale"), (v_descale, "v_descale")):
-        if t is not None:
-            _want(fp8, f"{n} belongs to an E4M3 cache")
-            _vec(t, n, torch.float32, device, numel=Hk)
+def _descale(t, name, fp8, Hk, index):
+    if t is None:
+        return None
+    if not fp8:
+        raise ValueError(f"{name} belongs to an E4M3 cache")
+    return _vec(t, name, _F32, index, Hk)
 
 
 def paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps: float = 1e-6,
@@ -645,32 +658,28 @@ def paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps:
     """qk_norm_rope for T new tokens, q [T,Hq,d], k, v [T,Hk,d] (bf16, strided views allowed), with k
     and v written to the paged cache at ``slots`` (int64 [T]; negative: the token is skipped and
     its row of q_out stays as it was).  Returns q_out [T,Hq,d]."""
-    _rows(q, "q", 3)
-    dev = q.device
-    _rows(k, "k", 3, dev)
-    _rows(v, "v", 3, dev)
-    T, Hq, d = q.shape
-    fp8, pages, ps, Hk, dc, cst = _cache(k_cache, v_cache, dev)
-    _want(k.shape == (T, Hk, d) and v.shape == k.shape and dc == d,
-          "k and v must be [T,Hk,d] with the cache's Hk and q's T and d")
-    _weights(wq, wk, d, dev)
-    rope, rows, rot = _rope_args(rope, d, dev)
-    if positions is not None:
-        _vec(positions, "positions", torch.int32, dev, numel=T)
-    else:
-        _want(rot == 0, "positions are needed for the rotation")
-    _vec(slots, "slots", torch.int64, dev, numel=T)
+    T, Hq, d = _rows(q, "q", 3, None)
+    index = q.get_device()
+    fp8, (pages, page_size, Hk, dc), strides = _cache(k_cache, v_cache, index)
+    if _rows(k, "k", 3, index) != (T, Hk, d) or _rows(v, "v", 3, index) != (T, Hk, d) or dc != d:
+        raise ValueError("k and v must be [T,Hk,d] with the cache's Hk and q's T and d")
     _distinct(k_cache, "k_cache")
     _distinct(v_cache, "v_cache")
-    _descales(k_descale, v_descale, fp8, Hk, dev)
-    if q_out is None:
-        q_out = torch.empty((T, Hq, d), device=dev, dtype=torch.bfloat16)
-    else:
-        _vec(q_out, "q_out", torch.bfloat16, dev, shape=(T, Hq, d))
-    _run(fa_paged_append, "fa_paged_append", dev, q, k, v, wq, wk, rope, rows, rot, interleaved, positions, slots, q_out,
-         k_cache, v_cache, fp8, k_descale, v_descale, pages, ps, T, Hq, Hk, d, _strides(q), _strides(k), _strides(v),
-         cst, eps)
+    table, rows, rot = _rope(rope, index)
+    if positions is not None:
+        positions = _vec(positions, "positions", _I32, index, T)
+    elif rot:
+        raise ValueError("positions are needed for the rotation")
+    q_out = _out(q_out, "q_out", _BF16, q.device, index, (T, Hq, d))
+    _call("fa_paged_append", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), _weight(wq, "wq", d, index),
+          _weight(wk, "wk", d, index), table, rows, rot, interleaved, positions, _vec(slots, "slots", _I64, index, T),
+          q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), fp8, _descale(k_descale, "k_descale", fp8, Hk, index),
+          _descale(v_descale, "v_descale", fp8, Hk, index), pages, page_size, T, Hq, Hk, d, *q.stride()[:2],
+          *k.stride()[:2], *v.stride()[:2], *strides[:3], eps)
     return q_out
+
+
+_decode_workspace = {}  # bytes that fa_paged_decode needs, by device (they depend on its SMs alone)
 
 
 def paged_decode(q, k_cache, v_cache, block_table, lens, scale: float | None = None, req=None, k_descale=None,
@@ -678,27 +687,22 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, scale: float | None = N
     """O [T,Hq,d] (bf16), LSE [T,Hq] of one query token per row, q [T,Hq,d], over the paged cache: row
     t sees lens[t] keys (int32, on the device) of row req[t] of the block table (int32; None: of
     row t; negative: the output row stays as it was).  A row with no key gets O = 0, LSE = -inf."""
-    _rows(q, "q", 3)
-    dev = q.device
-    T, Hq, d = q.shape
-    fp8, pages, ps, Hk, dc, cst = _cache(k_cache, v_cache, dev)
-    _want(dc == d and Hk > 0 and Hq % Hk == 0, "q's heads must be a multiple of the cache's, with its d")
-    stride = _table(block_table, dev)
-    _vec(lens, "lens", torch.int32, dev, numel=T)
-    if req is not None:
-        _vec(req, "req", torch.int32, dev, numel=T)
-    _descales(k_descale, v_descale, fp8, Hk, dev)
-    if out is None:
-        out = torch.empty((T, Hq, d), device=dev, dtype=torch.bfloat16)
-    else:
-        _vec(out, "out", torch.bfloat16, dev, shape=(T, Hq, d))
-    if lse is None:
-        lse = torch.empty((T, Hq), device=dev, dtype=torch.float32)
-    else:
-        _vec(lse, "lse", torch.float32, dev, shape=(T, Hq))
-    with _current(dev):
-        workspace = _workspace(workspace, fa_paged_decode_workspace_bytes(T, Hq, Hk, d), dev)
-    _run(fa_paged_decode, "fa_paged_decode", dev, q, k_cache, v_cache, fp8, k_descale, v_descale, block_table, stride,
-         block_table.shape[0], block_table.shape[1], lens, req, out, lse, workspace, workspace.numel(), pages, ps, T, Hq,
-         Hk, d, _strides(q), cst, d ** -0.5 if scale is None else scale)
+    T, Hq, d = _rows(q, "q", 3, None)
+    index, dev = q.get_device(), q.device
+    fp8, (pages, page_size, Hk, dc), strides = _cache(k_cache, v_cache, index)
+    if dc != d or Hk == 0 or Hq % Hk:
+        raise ValueError("q's heads must be a multiple of the cache's, with its d")
+    table, stride, rows, cols = _table(block_table, index)
+    out = _out(out, "out", _BF16, dev, index, (T, Hq, d))
+    lse = _out(lse, "lse", _F32, dev, index, (T, Hq))
+    nbytes = _decode_workspace.get(index)
+    if nbytes is None:
+        with torch.cuda.device(index):
+            nbytes = _decode_workspace[index] = fa_paged_decode_workspace_bytes(1, 1, 1, 64)
+    workspace = _workspace(workspace, nbytes, dev, index)
+    _call("fa_paged_decode", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), fp8,
+          _descale(k_descale, "k_descale", fp8, Hk, index), _descale(v_descale, "v_descale", fp8, Hk, index), table, stride,
+          rows, cols, _vec(lens, "lens", _I32, index, T), None if req is None else _vec(req, "req", _I32, index, T),
+          out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), pages, page_size, T, Hq, Hk, d,
+          *q.stride()[:2], *strides[:3], d ** -0.5 if scale is None else scale)
     return out, lse

@@ -104,8 +104,8 @@ REFUSALS = [
     (dict(inter=2), INVALID), (dict(d=32, rot=0), UNSUPPORTED), (dict(d=256), UNSUPPORTED),
     (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
     (dict(B=-1), INVALID), (dict(N=-1), INVALID), (dict(Hq=-1), INVALID), (dict(Hk=-1), INVALID),
-    (dict(qs=(8192, 128, 60)), INVALID), (dict(qs=(8192, 4, 64)), INVALID), (dict(ks=(8190, 64, 64)), INVALID),
-    (dict(qs=(1 << 62, 128, 64)), INVALID), (dict(B=1 << 16, N=1 << 16), INVALID),
+    (dict(qs=(8192, 128, 60)), INVALID), (dict(qs=(8192, 4, 64)), INVALID), (dict(B=2, ks=(8190, 64, 64)), INVALID),
+    (dict(B=2, qs=(1 << 60, 128, 64)), INVALID), (dict(B=1 << 16, N=1 << 16), INVALID),
 ]
 
 
