@@ -24,7 +24,8 @@ using namespace ptx;
 // padding when the step cannot be planned.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxCtas = 8;
-constexpr int kPlanTokensPerThread = 4;
+constexpr int kPlanTokens = 4;  // neighbouring tokens per thread: one search, one wide store per output
+constexpr int kPlanBatch = 8;
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -42,6 +43,11 @@ __device__ __forceinline__ Sum3 shfl_up3(const Sum3& a, int o) {
           __shfl_up_sync(0xffffffffu, a.back, o)};
 }
 
+// n / page_size for 0 <= n < 2^31 (see page_division).
+__device__ __forceinline__ int div_page(int n, uint64_t mul, int shift) {
+  return (int)(((uint64_t)(uint32_t)n * mul) >> shift);
+}
+
 __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanArgs a) {
   // per request: cached length (complemented when released), first wanted or released page in
   // the step's order, first token
@@ -51,14 +57,16 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
   int* s_cu = sm + 2 * a.R;  // R + 1
   __shared__ Sum3 warp_sum[32];
   __shared__ Sum3 carry;
+  __shared__ int s_bits;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
   const int rank = blockIdx.x, ctas = gridDim.x;  // the grid is one cluster
   const int ps = a.page_size;
   const long long room = (long long)a.table_cols * ps;
+  auto pages_of = [&](int n) { return n == 0 ? 0 : div_page(n - 1, a.page_mul, a.page_shift) + 1; };
 
   const int free0 = *a.free_count;
   int bits = 0;
-  if (tid == 0) carry = {0, 0, 0};
+  if (tid == 0) carry = {0, 0, 0}, s_bits = 0;
   __syncthreads();
   for (int base = 0; base < a.R; base += nt) {
     const int b = base + tid;
@@ -71,14 +79,14 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
         bits |= FA_PLAN_BAD_INPUT;
         cached = 0, add = 0;
       }
-      const int used = (int)(((long long)cached + ps - 1) / ps);
+      const int used = pages_of(cached);
       if (add < 0) {
         v.back = used;
       } else if ((long long)cached + add > room) {
         bits |= FA_PLAN_ROW_FULL;
       } else {
         v.grow = add;
-        v.want = ((long long)cached + add + ps - 1) / ps - used;
+        v.want = pages_of(cached + add) - used;
       }
     }
     Sum3 x = v;  // inclusive scan over the block
@@ -109,15 +117,15 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
     }
     __syncthreads();
     if (tid == 0) carry = carry + warp_sum[nw - 1];
+    if (base + nt >= a.R && bits) atomicOr(&s_bits, bits);
     __syncthreads();
   }
   const Sum3 total = carry;
+  bits = s_bits;
   const long long avail = free0 + total.back;
   if (free0 < 0 || avail > a.pool_pages) bits |= FA_PLAN_BAD_INPUT;
   else if (total.want > avail) bits |= FA_PLAN_NO_PAGES;
   if (total.grow > a.max_tokens) bits |= FA_PLAN_TOO_MANY_TOKENS;
-  bits = (__syncthreads_or(bits & 1) ? 1 : 0) | (__syncthreads_or(bits & 2) ? 2 : 0) |
-         (__syncthreads_or(bits & 4) ? 4 : 0) | (__syncthreads_or(bits & 8) ? 8 : 0);
   const bool ok = bits == 0;
   const int tokens = ok ? (int)total.grow : 0;
   if (tid == 0) s_cu[a.R] = tokens;
@@ -134,10 +142,18 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
     for (int b = rank * nw + warp; b < a.R; b += ctas * nw) {
       const int c = s_cached[b];
       if (c >= 0) continue;
-      const int used = (int)(((long long)~c + ps - 1) / ps);
+      const int used = pages_of(~c);
       const int* row = a.table + (long long)b * a.table_stride;
       int* top = a.free_pages + free0 + s_first[b];
-      for (int p = lane; p < used; p += 32) top[p] = row[p];
+      for (int p0 = lane; p0 < used; p0 += 32 * kPlanBatch) {
+        int page[kPlanBatch];
+#pragma unroll
+        for (int i = 0; i < kPlanBatch; ++i)
+          if (p0 + 32 * i < used) page[i] = row[p0 + 32 * i];
+#pragma unroll
+        for (int i = 0; i < kPlanBatch; ++i)
+          if (p0 + 32 * i < used) top[p0 + 32 * i] = page[i];
+      }
     }
     if (ctas > 1) cluster_sync();
     else __syncthreads();
@@ -148,32 +164,49 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
     a.cu_tokens[b] = ok ? s_cu[b] : 0;
   }
   const int top = (int)(avail - 1);
-  for (int t = gt; t < a.max_tokens; t += gn) {
-    long long slot = -1;
-    int pos = 0, req = -1;
-    if (t < tokens) {
-      int lo = 0, hi = a.R;  // the request with cu[lo] <= t < cu[lo + 1]
+  for (int t0 = gt * kPlanTokens; t0 < a.max_tokens; t0 += gn * kPlanTokens) {
+    int lo = 0;
+    if (t0 < tokens) {
+      int hi = a.R;  // the request with cu[lo] <= t0 < cu[lo + 1]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_cu[mid] <= t) lo = mid;
+        if (s_cu[mid] <= t0) lo = mid;
         else hi = mid;
       }
-      req = lo;
-      const int c = s_cached[lo];
-      pos = c + t - s_cu[lo];
-      const int p = pos / ps, used = (int)(((long long)c + ps - 1) / ps), in = pos - p * ps;
-      int page;
-      if (p < used) {
-        page = a.table[(long long)lo * a.table_stride + p];
-      } else {  // a page of this step; its first token enters it in the table
-        page = a.free_pages[top - (s_first[lo] + p - used)];
-        if (in == 0) a.table[(long long)lo * a.table_stride + p] = page;
-      }
-      slot = (long long)page * ps + in;
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
-    a.token_req[t] = req;
+    int pos[kPlanTokens], req[kPlanTokens], page[kPlanTokens], in[kPlanTokens];
+    int* enter[kPlanTokens];
+#pragma unroll
+    for (int i = 0; i < kPlanTokens; ++i) {
+      const int t = t0 + i;
+      pos[i] = 0, req[i] = -1, page[i] = -1, in[i] = 0, enter[i] = nullptr;
+      if (t < tokens) {
+        while (s_cu[lo + 1] <= t) ++lo;
+        req[i] = lo;
+        const int c = s_cached[lo], used = pages_of(c);
+        pos[i] = c + t - s_cu[lo];
+        const int p = div_page(pos[i], a.page_mul, a.page_shift);
+        in[i] = pos[i] - p * ps;
+        int* entry = a.table + (long long)lo * a.table_stride + p;
+        if (p >= used && in[i] == 0) enter[i] = entry;  // the first token of a page of this step
+        page[i] = p < used ? *entry : a.free_pages[top - (s_first[lo] + p - used)];
+      }
+    }
+    long long slot[kPlanTokens];
+#pragma unroll
+    for (int i = 0; i < kPlanTokens; ++i) {
+      slot[i] = t0 + i < tokens ? (long long)page[i] * ps + in[i] : -1;
+      if (enter[i]) *enter[i] = page[i];
+    }
+    if (a.wide && t0 + kPlanTokens <= a.max_tokens) {
+      *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.token_req + t0) = make_int4(req[0], req[1], req[2], req[3]);
+    } else {
+      for (int i = 0; i < kPlanTokens && t0 + i < a.max_tokens; ++i)
+        a.slots[t0 + i] = slot[i], a.positions[t0 + i] = pos[i], a.token_req[t0 + i] = req[i];
+    }
   }
 }
 
@@ -459,7 +492,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
     const int key = (ahead.tile << shift) + my_key;
     off = -1;
     if (fetch_left > 0 && key < ahead.len) {
-      const int p = (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift);  // key / page_size
+      const int p = div_page(key, a.page_mul, a.page_shift);
       const int page = __ldg(a.table + (long long)ahead.r * a.table_stride + p);
       if (page < 0 || page >= a.num_pages) atomicOr(a.status, FA_DEV_BOUNDS);
       else off = page * a.c_sp + (key - p * a.page_size) * a.c_st;
@@ -875,7 +908,19 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
+// n / page_size = n * mul >> shift for every n < 2^31 (Granlund and Montgomery, "Division by Invariant
+// Integers using Multiplication").
+static void page_division(int page_size, uint64_t* mul, int* shift) {
+  int bits = 0;
+  while ((1LL << bits) < page_size) ++bits;
+  *shift = 31 + bits;
+  *mul = (uint64_t)((((unsigned __int128)1 << *shift) + page_size - 1) / page_size);
+}
+
+cudaError_t launch_paged_plan(PlanArgs a, cudaStream_t stream) {
+  page_division(a.page_size, &a.page_mul, &a.page_shift);
+  a.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions) |
+             reinterpret_cast<uintptr_t>(a.token_req)) & 15) == 0;
   const int smem = (3 * a.R + 1) * 4;
   if (smem > 48 * 1024) {
     static bool attr_set[64];
@@ -889,9 +934,9 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t stream) {
       if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
   }
-  const long long share = (long long)kPlanThreads * kPlanTokensPerThread;
+  const long long share = (long long)kPlanThreads * kPlanTokens;
   const int ctas = (int)std::min<long long>(kPlanMaxCtas, std::max<long long>(1, (a.max_tokens + share - 1) / share));
-  const int need = std::max(a.R, ctas > 1 ? kPlanThreads : a.max_tokens);
+  const int need = std::max(a.R, ctas > 1 ? kPlanThreads : (a.max_tokens + kPlanTokens - 1) / kPlanTokens);
   const int threads = std::min(kPlanThreads, std::max(64, (need + 31) / 32 * 32));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
@@ -914,12 +959,7 @@ size_t paged_decode_workspace(int T, int Hq, int Hk, int d) {
 }
 
 cudaError_t launch_paged_decode(int d, bool fp8, DecodeArgs a, cudaStream_t stream) {
-  // key / page_size = key * page_mul >> page_shift for every key < 2^31 (Granlund and Montgomery,
-  // "Division by Invariant Integers using Multiplication")
-  int bits = 0;
-  while ((1LL << bits) < a.page_size) ++bits;
-  a.page_shift = 31 + bits;
-  a.page_mul = (uint64_t)((((unsigned __int128)1 << a.page_shift) + a.page_size - 1) / a.page_size);
+  page_division(a.page_size, &a.page_mul, &a.page_shift);
   // Heads side by side: when a token's heads follow one another, as many as make up 256 bytes are read
   // at once; pieces of 128 bytes read alone, at different times, reach a tenth less bandwidth.
   const int row_bytes = d * (fp8 ? 1 : 2);

@@ -450,13 +450,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _new(shape, dtype, device):
-    """torch.empty (contiguous) by the shorter way."""
-    strides, n = [], 1
-    for size in reversed(shape):
-        strides.append(n)
-        n *= max(size, 1)
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+_new = torch.empty_strided  # torch.empty by a shorter way
 
 
 def _call(name, index, *args):
@@ -488,13 +482,10 @@ def _vec(t, name, dtype, index, numel):
     return t.data_ptr()
 
 
-def _out(t, name, dtype, device, index, shape):
-    """An output: the caller's contiguous tensor, checked, or a new one."""
-    if t is None:
-        return _new(shape, dtype, device)
+def _out(t, name, dtype, index, shape):
+    """The caller's output, checked."""
     if not (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on CUDA device {index}")
-    return t
 
 
 def _distinct(t, name):
@@ -512,7 +503,7 @@ def _distinct(t, name):
 def _workspace(t, nbytes, device, index):
     """The caller's workspace, checked, or a new one."""
     if t is None:
-        return _new((max(nbytes, 256),), _U8, device)
+        return _new((max(nbytes, 256),), (1,), dtype=_U8, device=device)
     if t.dtype is not _U8 or t.get_device() != index or not t.is_contiguous() or t.numel() < nbytes:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on CUDA device {index}")
     return t
@@ -562,8 +553,14 @@ def qk_norm_rope(q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interlea
     B, N, Hq, Hk, d, dev, index = _qk(q, k)
     table, rows, rot = _rope(rope, index)
     pos, pos_sb = _positions(positions, B, N, index)
-    q_out = _out(q_out, "q_out", _BF16, dev, index, (B, Hq, N, d))
-    k_out = _out(k_out, "k_out", _BF16, dev, index, (B, Hk, N, d))
+    if q_out is None:
+        q_out = _new((B, Hq, N, d), (Hq * N * d, N * d, d, 1), dtype=_BF16, device=dev)
+    else:
+        _out(q_out, "q_out", _BF16, index, (B, Hq, N, d))
+    if k_out is None:
+        k_out = _new((B, Hk, N, d), (Hk * N * d, N * d, d, 1), dtype=_BF16, device=dev)
+    else:
+        _out(k_out, "k_out", _BF16, index, (B, Hk, N, d))
     _call("fa_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), _weight(wq, "wq", d, index),
           _weight(wk, "wk", d, index), table, rows, rot, interleaved, pos, pos_sb, q_out.data_ptr(), k_out.data_ptr(),
           B, N, Hq, Hk, d, *q.stride()[:3], *k.stride()[:3], eps)
@@ -581,18 +578,18 @@ def qk_norm_rope_backward(gq, gk, q, k, wq, wk, rope, positions=None, eps: float
     table, rows, rot = _rope(rope, index)
     pos, pos_sb = _positions(positions, B, N, index)
     if dq is None:
-        dq = _new((B, N, Hq, d), _BF16, dev)
+        dq = _new((B, N, Hq, d), (N * Hq * d, Hq * d, d, 1), dtype=_BF16, device=dev)
     elif _rows(dq, "dq", 4, index) != q.shape:
         raise ValueError(f"dq must have the shape {tuple(q.shape)}")
     else:
         _distinct(dq, "dq")
     if dk is None:
-        dk = _new((B, N, Hk, d), _BF16, dev)
+        dk = _new((B, N, Hk, d), (N * Hk * d, Hk * d, d, 1), dtype=_BF16, device=dev)
     elif _rows(dk, "dk", 4, index) != k.shape:
         raise ValueError(f"dk must have the shape {tuple(k.shape)}")
     else:
         _distinct(dk, "dk")
-    dwq, dwk = _new((d,), _F32, dev), _new((d,), _F32, dev)
+    dwq, dwk = (_new((d,), (1,), dtype=_F32, device=dev) for _ in range(2))
     workspace = _workspace(workspace, fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d), dev, index)
     _call("fa_qk_norm_rope_bwd", index, _vec(gq, "gq", _BF16, index, B * Hq * N * d),
           _vec(gk, "gk", _BF16, index, B * Hk * N * d), q.data_ptr(), k.data_ptr(), _weight(wq, "wq", d, index),
@@ -670,7 +667,10 @@ def paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps:
         positions = _vec(positions, "positions", _I32, index, T)
     elif rot:
         raise ValueError("positions are needed for the rotation")
-    q_out = _out(q_out, "q_out", _BF16, q.device, index, (T, Hq, d))
+    if q_out is None:
+        q_out = _new((T, Hq, d), (Hq * d, d, 1), dtype=_BF16, device=q.device)
+    else:
+        _out(q_out, "q_out", _BF16, index, (T, Hq, d))
     _call("fa_paged_append", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), _weight(wq, "wq", d, index),
           _weight(wk, "wk", d, index), table, rows, rot, interleaved, positions, _vec(slots, "slots", _I64, index, T),
           q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), fp8, _descale(k_descale, "k_descale", fp8, Hk, index),
@@ -693,8 +693,14 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, scale: float | None = N
     if dc != d or Hk == 0 or Hq % Hk:
         raise ValueError("q's heads must be a multiple of the cache's, with its d")
     table, stride, rows, cols = _table(block_table, index)
-    out = _out(out, "out", _BF16, dev, index, (T, Hq, d))
-    lse = _out(lse, "lse", _F32, dev, index, (T, Hq))
+    if out is None:
+        out = _new((T, Hq, d), (Hq * d, d, 1), dtype=_BF16, device=dev)
+    else:
+        _out(out, "out", _BF16, index, (T, Hq, d))
+    if lse is None:
+        lse = _new((T, Hq), (Hq, 1), dtype=_F32, device=dev)
+    else:
+        _out(lse, "lse", _F32, index, (T, Hq))
     nbytes = _decode_workspace.get(index)
     if nbytes is None:
         with torch.cuda.device(index):
