@@ -4,6 +4,9 @@ visit counters, see include/fa.h).
 
     python -m io_aware_exact_22_b200.build [--force] [--verbose] [--debug | --all]
 
+libfa.so comes with _fa_torch.so, the extension of the binding (csrc/fa_torch.cpp, host code only,
+compiled against the torch that runs the build).
+
 Each .cu file under csrc/ is compiled to an object in _build/ (skipped when the object is
 newer than every source and header), then linked into one shared library against the static
 CUDA runtime.  The tensor-map encoder is fetched from the driver at run time, so the library
@@ -27,6 +30,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 BUILD_DEBUG = os.path.join(ROOT, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libfa_debug.so")
+
+EXT_SRC = os.path.join(CSRC, "fa_torch.cpp")
+EXT = os.path.join(PKG, "_fa_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -53,6 +59,27 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_ext(force: bool, verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    if not force and not _stale(EXT, [EXT_SRC, os.path.join(INCLUDE, "fa.h"), torch.__file__]):
+        return
+    # nvcc, for its host compiler and CUDA's headers (the one in CXX may come with another C++ runtime)
+    cmd = [nvcc(), "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-o", EXT, EXT_SRC, "-I" + INCLUDE,
+           *("-I" + os.path.join(base, "include", *d) for d in ((), ("torch", "csrc", "api", "include"))),
+           "-I" + sysconfig.get_paths()["include"], f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, debug: bool = False) -> str:
@@ -93,6 +120,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False, deb
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
+    if not debug:
+        _build_ext(force, verbose)
     return lib
 
 

@@ -7,8 +7,8 @@ torch tensors supply device pointers and the current CUDA stream, and every step
 attention path runs in the library's kernels.  ``forward``, ``forward_splitkv``,
 ``forward_fp8``, ``backward``, ``qk_norm_rope``, ``qk_norm_rope_backward``, ``paged_plan``,
 ``paged_append`` and ``paged_decode`` additionally check their tensors and allocate the outputs
-that are not given with torch (memory plumbing only); the last five run on the tensors' device,
-on its current stream.
+that are not given with torch (memory plumbing only); the last five do so in a small extension
+(csrc/fa_torch.cpp), on the tensors' device and its current stream.
 
 Loading fails loudly (``RuntimeError``) when the shared library is missing: there is no
 fallback implementation.
@@ -441,106 +441,31 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, device="cuda"):
     return torch.stack([ang.cos(), ang.sin()], 1).float().contiguous()
 
 
-# The calls below are short enough on the device for the host to be what a caller waits for, so
-# their checks read each tensor's metadata once, and they hand the C functions addresses
-# themselves.  Strides go as they are: the library does not look at the stride of a dimension of
-# one element.
-_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The calls below are as short on the device as marshalling them in Python would be on the host, so
+# their tensors go to a small extension (csrc/fa_torch.cpp) that checks them, allocates the outputs
+# that are not given, and calls the C function on the tensors' device and its current stream.
+_ext = None
 
 
-_new = torch.empty_strided  # torch.empty by a shorter way
+def _load_ext():
+    """The extension, bound to the library that ``lib`` loads; raise RuntimeError if it is not built."""
+    global _ext
+    L = lib()
+    try:
+        from . import _fa_torch
+    except ImportError as e:
+        raise RuntimeError("_fa_torch.so not found beside fa.py, or not for this torch; build it with "
+                           "`python -m io_aware_exact_22_b200.build`") from e
+    _fa_torch.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in EXPORTS})
+    _ext = _fa_torch
+    return _ext
 
 
-def _call(name, index, *args):
-    """Calls a C function with device `index` current, on its current stream."""
-    fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, _raw_stream(index))
-    if rc:
-        raise FAError(rc, name)
-
-
-def _rows(t, name, dims, index):
-    """Shape of a bf16 tensor of `dims` dimensions on CUDA device `index` (any, if None), the last
-    one contiguous."""
-    shape = t.shape
-    if not (t.dtype is _BF16 and len(shape) == dims and t.is_cuda and (index is None or t.get_device() == index)
-            and (t.stride(-1) == 1 or shape[-1] <= 1)):
-        raise ValueError(f"{name} must be a bf16 tensor of {dims} dimensions, the last one contiguous, on one CUDA device")
-    return shape
-
-
-def _vec(t, name, dtype, index, numel):
-    """Address of a contiguous tensor of `dtype` and that many elements on CUDA device `index`."""
-    if not (t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.numel() == numel):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on CUDA device {index}")
-    return t.data_ptr()
-
-
-def _out(t, name, dtype, index, shape):
-    """The caller's output, checked."""
-    if not (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on CUDA device {index}")
-
-
-def _distinct(t, name):
-    """An output's elements must lie at addresses of their own (each stride past all that the smaller
-    ones reach)."""
-    if t.is_contiguous():
-        return
-    reach = 0
-    for st, n in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
-        if st <= reach:
-            raise ValueError(f"{name} must not overlap itself")
-        reach += st * (n - 1)
-
-
-def _workspace(t, nbytes, device, index):
-    """The caller's workspace, checked, or a new one."""
-    if t is None:
-        return _new((max(nbytes, 256),), (1,), dtype=_U8, device=device)
-    if t.dtype is not _U8 or t.get_device() != index or not t.is_contiguous() or t.numel() < nbytes:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {nbytes} bytes on CUDA device {index}")
-    return t
-
-
-def _weight(w, name, d, index):
-    return None if w is None else _vec(w, name, _BF16, index, d)
-
-
-def _rope(rope, index):
-    """(address, rows, rot) of a rope_table, or of None for no rotation."""
-    if rope is None:
-        return None, 0, 0
-    shape = rope.shape
-    if not (len(shape) == 3 and shape[1] == 2 and rope.dtype is _F32 and rope.get_device() == index
-            and rope.is_contiguous()):
-        raise ValueError(f"rope must be a contiguous fp32 table [rows, 2, rot/2] on CUDA device {index}")
-    return rope.data_ptr(), shape[0], 2 * shape[2]
-
-
-def _positions(positions, B, N, index):
-    """(address or None, batch stride) of int32 positions [N] or [B,N]."""
-    if positions is None:
-        return None, 0
-    shape = positions.shape
-    if not (positions.dtype is _I32 and positions.get_device() == index and (shape == (N,) or shape == (B, N))
-            and (N <= 1 or positions.stride(-1) == 1)):
-        raise ValueError(f"positions must be an int32 tensor [N] or [B,N], contiguous along N, on CUDA device {index}")
-    return positions.data_ptr(), positions.stride(0) if len(shape) == 2 else 0
-
-
-def _qk(q, k):
-    B, N, Hq, d = _rows(q, "q", 4, None)
-    index = q.get_device()
-    if _rows(k, "k", 4, index) != (B, N, k.shape[2], d):
-        raise ValueError("q [B,N,Hq,d] and k [B,N,Hk,d] must agree in B, N and d")
-    return B, N, Hq, k.shape[2], d, q.device, index
+def _result(r, name):
+    """What the extension returned; a C status other than FA_OK is an error."""
+    if type(r) is int and r:
+        raise FAError(r, name)
+    return r
 
 
 def qk_norm_rope(q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
@@ -550,21 +475,8 @@ def qk_norm_rope(q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interlea
     contiguous [B,Hq,N,d] and [B,Hk,N,d], the layout that ``forward`` reads.  wq, wk: bf16 [d] or
     None; rope: ``rope_table``'s or None for the norm alone; positions: int32 [N] or [B,N], or
     None for 0..N-1."""
-    B, N, Hq, Hk, d, dev, index = _qk(q, k)
-    table, rows, rot = _rope(rope, index)
-    pos, pos_sb = _positions(positions, B, N, index)
-    if q_out is None:
-        q_out = _new((B, Hq, N, d), (Hq * N * d, N * d, d, 1), dtype=_BF16, device=dev)
-    else:
-        _out(q_out, "q_out", _BF16, index, (B, Hq, N, d))
-    if k_out is None:
-        k_out = _new((B, Hk, N, d), (Hk * N * d, N * d, d, 1), dtype=_BF16, device=dev)
-    else:
-        _out(k_out, "k_out", _BF16, index, (B, Hk, N, d))
-    _call("fa_qk_norm_rope", index, q.data_ptr(), k.data_ptr(), _weight(wq, "wq", d, index),
-          _weight(wk, "wk", d, index), table, rows, rot, interleaved, pos, pos_sb, q_out.data_ptr(), k_out.data_ptr(),
-          B, N, Hq, Hk, d, *q.stride()[:3], *k.stride()[:3], eps)
-    return q_out, k_out
+    return _result((_ext or _load_ext()).qk_norm_rope(q, k, wq, wk, rope, positions, eps, interleaved, q_out, k_out),
+                   "fa_qk_norm_rope")
 
 
 def qk_norm_rope_backward(gq, gk, q, k, wq, wk, rope, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -572,39 +484,8 @@ def qk_norm_rope_backward(gq, gk, q, k, wq, wk, rope, positions=None, eps: float
     """dq, dk (bf16 [B,N,H,d]), dwq, dwk (fp32 [d]) from gq [B,Hq,N,d], gk [B,Hk,N,d], the
     gradients of qk_norm_rope's outputs (``backward``'s dq, dk); dq, dk may be given as views, for
     instance of a fused projection's gradient."""
-    B, N, Hq, Hk, d, dev, index = _qk(q, k)
-    if gq.shape != (B, Hq, N, d) or gk.shape != (B, Hk, N, d):
-        raise ValueError("gq and gk must be [B,Hq,N,d] and [B,Hk,N,d]")
-    table, rows, rot = _rope(rope, index)
-    pos, pos_sb = _positions(positions, B, N, index)
-    if dq is None:
-        dq = _new((B, N, Hq, d), (N * Hq * d, Hq * d, d, 1), dtype=_BF16, device=dev)
-    elif _rows(dq, "dq", 4, index) != q.shape:
-        raise ValueError(f"dq must have the shape {tuple(q.shape)}")
-    else:
-        _distinct(dq, "dq")
-    if dk is None:
-        dk = _new((B, N, Hk, d), (N * Hk * d, Hk * d, d, 1), dtype=_BF16, device=dev)
-    elif _rows(dk, "dk", 4, index) != k.shape:
-        raise ValueError(f"dk must have the shape {tuple(k.shape)}")
-    else:
-        _distinct(dk, "dk")
-    dwq, dwk = (_new((d,), (1,), dtype=_F32, device=dev) for _ in range(2))
-    workspace = _workspace(workspace, fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d), dev, index)
-    _call("fa_qk_norm_rope_bwd", index, _vec(gq, "gq", _BF16, index, B * Hq * N * d),
-          _vec(gk, "gk", _BF16, index, B * Hk * N * d), q.data_ptr(), k.data_ptr(), _weight(wq, "wq", d, index),
-          _weight(wk, "wk", d, index), table, rows, rot, interleaved, pos, pos_sb, dq.data_ptr(), dk.data_ptr(),
-          dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(), B, N, Hq, Hk, d, *q.stride()[:3],
-          *k.stride()[:3], *dq.stride()[:3], *dk.stride()[:3], eps)
-    return dq, dk, dwq, dwk
-
-
-def _table(t, index):
-    """(address, row stride, rows, columns) of a block table."""
-    shape = t.shape
-    if not (t.dtype is _I32 and t.get_device() == index and len(shape) == 2 and (shape[1] <= 1 or t.stride(1) == 1)):
-        raise ValueError(f"block_table must be an int32 tensor [rows, cols], its rows contiguous, on CUDA device {index}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1], *shape
+    return _result((_ext or _load_ext()).qk_norm_rope_backward(gq, gk, q, k, wq, wk, rope, positions, eps, interleaved,
+                                                               dq, dk, workspace), "fa_qk_norm_rope_bwd")
 
 
 def paged_plan(cached, new_tokens, block_table, free_pages, free_count, page_size: int, lens, cu_tokens, slots,
@@ -615,39 +496,9 @@ def paged_plan(cached, new_tokens, block_table, free_pages, free_count, page_siz
     token_req [max_tokens], free_count_out [1], status [1] out.  lens may be ``cached`` and
     free_count_out ``free_count``.  Nothing is read back: a step that cannot be planned leaves a
     non-zero status (PLAN_*) on the device, slots of -1 and everything else as it was."""
-    if not cached.is_cuda:
-        raise ValueError("cached must be a CUDA tensor")
-    index, R, most, pool = cached.get_device(), cached.numel(), slots.numel(), free_pages.numel()
-    table, stride, rows, cols = _table(block_table, index)
-    if rows != R:
-        raise ValueError("block_table must have a row for each request")
-    _call("fa_paged_plan", index, _vec(cached, "cached", _I32, index, R), _vec(new_tokens, "new_tokens", _I32, index, R),
-          table, stride, cols, _vec(free_pages, "free_pages", _I32, index, pool), pool,
-          _vec(free_count, "free_count", _I32, index, 1), page_size, R, most, _vec(lens, "lens", _I32, index, R),
-          _vec(cu_tokens, "cu_tokens", _I32, index, R + 1), _vec(slots, "slots", _I64, index, most),
-          _vec(positions, "positions", _I32, index, most), _vec(token_req, "token_req", _I32, index, most),
-          _vec(free_count_out, "free_count_out", _I32, index, 1), _vec(status, "status", _I32, index, 1))
-
-
-def _cache(k_cache, v_cache, index):
-    """(fp8, shape, strides) of the two pools."""
-    shape, strides, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
-    if not (len(shape) == 4 and v_cache.shape == shape and v_cache.dtype is dtype
-            and (dtype is _BF16 or dtype is torch.float8_e4m3fn or dtype is _U8) and strides[3] == 1
-            and k_cache.get_device() == index and v_cache.get_device() == index):
-        raise ValueError("k_cache, v_cache must be bf16 or E4M3 tensors [pages, page_size, Hk, d] of one shape, the last "
-                         f"dimension contiguous, on CUDA device {index}")
-    if v_cache.stride() != strides:
-        raise ValueError("k_cache and v_cache must have the same strides")
-    return dtype is not _BF16, shape, strides
-
-
-def _descale(t, name, fp8, Hk, index):
-    if t is None:
-        return None
-    if not fp8:
-        raise ValueError(f"{name} belongs to an E4M3 cache")
-    return _vec(t, name, _F32, index, Hk)
+    _result((_ext or _load_ext()).paged_plan(cached, new_tokens, block_table, free_pages, free_count, page_size, lens,
+                                             cu_tokens, slots, positions, token_req, free_count_out, status),
+            "fa_paged_plan")
 
 
 def paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps: float = 1e-6,
@@ -655,31 +506,8 @@ def paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps:
     """qk_norm_rope for T new tokens, q [T,Hq,d], k, v [T,Hk,d] (bf16, strided views allowed), with k
     and v written to the paged cache at ``slots`` (int64 [T]; negative: the token is skipped and
     its row of q_out stays as it was).  Returns q_out [T,Hq,d]."""
-    T, Hq, d = _rows(q, "q", 3, None)
-    index = q.get_device()
-    fp8, (pages, page_size, Hk, dc), strides = _cache(k_cache, v_cache, index)
-    if _rows(k, "k", 3, index) != (T, Hk, d) or _rows(v, "v", 3, index) != (T, Hk, d) or dc != d:
-        raise ValueError("k and v must be [T,Hk,d] with the cache's Hk and q's T and d")
-    _distinct(k_cache, "k_cache")
-    _distinct(v_cache, "v_cache")
-    table, rows, rot = _rope(rope, index)
-    if positions is not None:
-        positions = _vec(positions, "positions", _I32, index, T)
-    elif rot:
-        raise ValueError("positions are needed for the rotation")
-    if q_out is None:
-        q_out = _new((T, Hq, d), (Hq * d, d, 1), dtype=_BF16, device=q.device)
-    else:
-        _out(q_out, "q_out", _BF16, index, (T, Hq, d))
-    _call("fa_paged_append", index, q.data_ptr(), k.data_ptr(), v.data_ptr(), _weight(wq, "wq", d, index),
-          _weight(wk, "wk", d, index), table, rows, rot, interleaved, positions, _vec(slots, "slots", _I64, index, T),
-          q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), fp8, _descale(k_descale, "k_descale", fp8, Hk, index),
-          _descale(v_descale, "v_descale", fp8, Hk, index), pages, page_size, T, Hq, Hk, d, *q.stride()[:2],
-          *k.stride()[:2], *v.stride()[:2], *strides[:3], eps)
-    return q_out
-
-
-_decode_workspace = {}  # bytes that fa_paged_decode needs, by device (they depend on its SMs alone)
+    return _result((_ext or _load_ext()).paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps,
+                                                      interleaved, k_descale, v_descale, q_out), "fa_paged_append")
 
 
 def paged_decode(q, k_cache, v_cache, block_table, lens, scale: float | None = None, req=None, k_descale=None,
@@ -687,28 +515,6 @@ def paged_decode(q, k_cache, v_cache, block_table, lens, scale: float | None = N
     """O [T,Hq,d] (bf16), LSE [T,Hq] of one query token per row, q [T,Hq,d], over the paged cache: row
     t sees lens[t] keys (int32, on the device) of row req[t] of the block table (int32; None: of
     row t; negative: the output row stays as it was).  A row with no key gets O = 0, LSE = -inf."""
-    T, Hq, d = _rows(q, "q", 3, None)
-    index, dev = q.get_device(), q.device
-    fp8, (pages, page_size, Hk, dc), strides = _cache(k_cache, v_cache, index)
-    if dc != d or Hk == 0 or Hq % Hk:
-        raise ValueError("q's heads must be a multiple of the cache's, with its d")
-    table, stride, rows, cols = _table(block_table, index)
-    if out is None:
-        out = _new((T, Hq, d), (Hq * d, d, 1), dtype=_BF16, device=dev)
-    else:
-        _out(out, "out", _BF16, index, (T, Hq, d))
-    if lse is None:
-        lse = _new((T, Hq), (Hq, 1), dtype=_F32, device=dev)
-    else:
-        _out(lse, "lse", _F32, index, (T, Hq))
-    nbytes = _decode_workspace.get(index)
-    if nbytes is None:
-        with torch.cuda.device(index):
-            nbytes = _decode_workspace[index] = fa_paged_decode_workspace_bytes(1, 1, 1, 64)
-    workspace = _workspace(workspace, nbytes, dev, index)
-    _call("fa_paged_decode", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), fp8,
-          _descale(k_descale, "k_descale", fp8, Hk, index), _descale(v_descale, "v_descale", fp8, Hk, index), table, stride,
-          rows, cols, _vec(lens, "lens", _I32, index, T), None if req is None else _vec(req, "req", _I32, index, T),
-          out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), pages, page_size, T, Hq, Hk, d,
-          *q.stride()[:2], *strides[:3], d ** -0.5 if scale is None else scale)
-    return out, lse
+    return _result((_ext or _load_ext()).paged_decode(q, k_cache, v_cache, block_table, lens,
+                                                      q.shape[-1] ** -0.5 if scale is None else scale, req, k_descale,
+                                                      v_descale, out, lse, workspace), "fa_paged_decode")
