@@ -129,15 +129,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
   const bool ok = bits == 0;
   const int tokens = ok ? (int)total.grow : 0;
   if (tid == 0) s_cu[a.R] = tokens;
-  if (ctas > 1) cluster_sync();  // every block has read the inputs; nothing is written before
-  else __syncthreads();
-
+  __syncthreads();
   const int gt = rank * nt + tid, gn = ctas * nt;
-  if (gt == 0) {
-    *a.free_count_out = ok ? (int)(avail - total.want) : free0;
-    *a.plan_status = bits;
-    a.cu_tokens[a.R] = tokens;
-  }
   if (ok && total.back > 0) {  // released pages onto the stack, a warp per request
     for (int b = rank * nw + warp; b < a.R; b += ctas * nw) {
       const int c = s_cached[b];
@@ -155,8 +148,15 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
           if (p0 + 32 * i < used) top[p0 + 32 * i] = page[i];
       }
     }
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
+  }
+  // Every block has read the inputs (nothing that may be one of them is written before), and the
+  // released pages are on the stack.
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  if (gt == 0) {
+    *a.free_count_out = ok ? (int)(avail - total.want) : free0;
+    *a.plan_status = bits;
+    a.cu_tokens[a.R] = tokens;
   }
   for (int b = gt; b < a.R; b += gn) {
     const int c = s_cached[b];
@@ -469,13 +469,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
     }
   }
   __syncthreads();
-  Cursor cur;
-  cur.t = s_start[0];
-  cur.hm = s_start[1];
-  cur.tile = s_start[2];
-  cur.len = row_keys(a, cur.t, cur.r);
-  cur.tiles = tiles_of(cur.len, shift);
-  Cursor ahead = cur;  // the next tile to fetch
+  Cursor ahead;  // the next tile to fetch
+  ahead.t = s_start[0];
+  ahead.hm = s_start[1];
+  ahead.tile = s_start[2];
+  ahead.len = row_keys(a, ahead.t, ahead.r);
+  ahead.tiles = tiles_of(ahead.len, shift);
   int fetch_left = (int)(last - first);
   int left = fetch_left;
 
@@ -523,8 +522,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
     lookup();
   };
   lookup();
+  Cursor line[kStages];  // the tiles on their way, the one that is computed next in front
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) fetch(s);
+  for (int s = 0; s < kStages; ++s) {
+    line[s] = ahead;
+    fetch(s);
+  }
 
   // ---- computing.  The thread's share of S^T and O^T: query rows 8 n + 2 i4 + e of keys (or
   // columns) g8 and g8 + 8 of each 16.
@@ -533,48 +536,60 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
   float m[NQ][2], l[NQ][2];
   uint32_t qb[DC][NQ][2];
   float sc[NQ][2];  // factor from the product to base-2 scores
+  // The queries of c's (row, kv head), as stored.
+  auto load_q = [&](const Cursor& c) {
+    const int hg = NQ == 1 ? c.hm : c.hm / runs, row0 = (c.hm - hg * runs) * kMaxRows, rows = min(kMaxRows, g - row0);
+    const __nv_bfloat16* q0 = a.q + c.t * a.q_st + ((long long)(hg * a.hp + hw) * g + row0) * a.q_sh;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const bool live = 8 * n + g8 < rows;
+      const __nv_bfloat16* qr = q0 + (live ? 8 * n + g8 : 0) * a.q_sh;
+#pragma unroll
+      for (int s = 0; s < DC; ++s) {
+        if (FP8) {
+          const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(qr + 16 * s + 4 * i4)) : make_uint2(0, 0);
+          qb[s][n][0] = v.x, qb[s][n][1] = v.y;
+        } else {
+          qb[s][n][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 2 * i4)) : 0u;
+          qb[s][n][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 8 + 2 * i4)) : 0u;
+        }
+      }
+    }
+  };
+  load_q(line[0]);
   int stage = 0;
   bool fresh = true;
-  int seg_tile0 = cur.tile;
+  int seg_tile0 = line[0].tile;
   while (left > 0) {
+    const Cursor cur = line[0];
     const int hg = NQ == 1 ? cur.hm : cur.hm / runs, hk = hg * a.hp + hw;
     const int row0 = (cur.hm - hg * runs) * kMaxRows, rows = min(kMaxRows, g - row0);
-    if (fresh) {  // this (row, kv head)'s queries, and an empty result
+    if (fresh) {  // a (row, kv head) begins: its queries are in qb
       fresh = false;
       seg_tile0 = cur.tile;
-      const __nv_bfloat16* q0 = a.q + cur.t * a.q_st + (long long)(hk * g + row0) * a.q_sh;
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const int row = 8 * n + g8;
-        const bool live = row < rows;
-        const __nv_bfloat16* qr = q0 + (live ? row : 0) * a.q_sh;
         if (!FP8) {
-#pragma unroll
-          for (int s = 0; s < DC; ++s) {
-            qb[s][n][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 2 * i4)) : 0u;
-            qb[s][n][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * s + 8 + 2 * i4)) : 0u;
-          }
           sc[n][0] = sc[n][1] = a.scale_log2;
         } else {
           // q to fp16 exactly but for elements 2^-24 below the row's largest: the row is scaled
           // by a power of two that brings that one into [1, 2)
-          uint2 v[DC];
           float big = 0.f;
 #pragma unroll
-          for (int s = 0; s < DC; ++s) {
-            v[s] = live ? __ldg(reinterpret_cast<const uint2*>(qr + 16 * s + 4 * i4)) : make_uint2(0, 0);
-            big = fmaxf(big, fmaxf(fmaxf(fabsf(__uint_as_float(v[s].x << 16)), fabsf(__uint_as_float(v[s].x & 0xffff0000u))),
-                                   fmaxf(fabsf(__uint_as_float(v[s].y << 16)), fabsf(__uint_as_float(v[s].y & 0xffff0000u)))));
-          }
+          for (int s = 0; s < DC; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              big = fmaxf(big, fmaxf(fabsf(__uint_as_float(qb[s][n][e] << 16)), fabsf(__uint_as_float(qb[s][n][e] & 0xffff0000u))));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
           const int e = min(max((int)(__float_as_uint(big) >> 23), 2), 252);  // biased exponent
           const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
 #pragma unroll
-          for (int s = 0; s < DC; ++s) {
-            qb[s][n][0] = pack_f16(__uint_as_float(v[s].x << 16) * down, __uint_as_float(v[s].x & 0xffff0000u) * down);
-            qb[s][n][1] = pack_f16(__uint_as_float(v[s].y << 16) * down, __uint_as_float(v[s].y & 0xffff0000u) * down);
-          }
+          for (int s = 0; s < DC; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              qb[s][n][e] = pack_f16(__uint_as_float(qb[s][n][e] << 16) * down,
+                                     __uint_as_float(qb[s][n][e] & 0xffff0000u) * down);
           const float f = a.scale_log2 * (a.kd ? __ldg(a.kd + hk) : 1.f) * up;
           sc[n][0] = __shfl_sync(0xffffffffu, f, 8 * i4);
           sc[n][1] = __shfl_sync(0xffffffffu, f, 8 * i4 + 4);
@@ -705,6 +720,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
 
     const bool seg_end = cur.tile + 1 == cur.tiles;
     if (seg_end || left == 0) {  // join the warps, 8 rows at a time
+      if (left > 0) load_q(line[1]);  // on their way meanwhile
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -770,12 +786,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
     } else {
       __syncwarp();  // all lanes have read the stage that is filled next
     }
+#pragma unroll
+    for (int s = 0; s + 1 < kStages; ++s) line[s] = line[s + 1];
+    line[kStages - 1] = ahead;
     fetch(stage);
     stage = stage == kStages - 1 ? 0 : stage + 1;
     if (left == 0) {
       if (tid == 0 && !by_group && seg_tile0 != 0) part.head[cta] = make_int4(-1, 0, 0, 0);  // no group began last
-    } else {
-      cursor_next(a, cur, groups, shift);
     }
   }
   cp_wait<0>();
