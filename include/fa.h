@@ -409,7 +409,7 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  * row's results; an infinite value makes its column infinite or NaN.  Equal calls give equal bits.
  * Empty problems (T or R 0 with nothing to write, Hq + Hk 0) return FA_OK; errors as elsewhere.
  */
-#define FA_PLAN_MAX_REQUESTS 16384
+#define FA_PLAN_MAX_REQUESTS 12288
 #define FA_PAGED_MAX_LEN 2147418112 /* 2^31 - 2^16 */
 #define FA_PLAN_NO_PAGES 1
 #define FA_PLAN_ROW_FULL 2

@@ -176,7 +176,7 @@ struct PlanArgs {
   long long table_stride;
   int table_cols, pool_pages, page_size, R, max_tokens;
   uint64_t page_mul;                 // set by the launcher: division by page_size
-  int page_shift, wide;              // wide: outputs per token are 16-byte aligned
+  int page_shift, wide;              // wide: the outputs per token are 16-byte aligned
 };
 cudaError_t launch_paged_plan(PlanArgs a, cudaStream_t stream);
 

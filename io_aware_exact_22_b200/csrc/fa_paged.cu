@@ -24,8 +24,11 @@ using namespace ptx;
 // padding when the step cannot be planned.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxCtas = 8;
-constexpr int kPlanTokens = 4;  // neighbouring tokens per thread: one search, one wide store per output
-constexpr int kPlanBatch = 8;
+constexpr int kPlanRequests = 256;  // at most, per block: with released pages 1000 requests take 8.3 us on 4, 10.3 on 1
+// Neighbouring tokens (or pages) per thread: one search, one store per output.  1000 requests with
+// 50 k tokens take 12.0 us with 2, 14.2 with 1, 12.4 with 4 and 16.9 with 8 (the longer chain of
+// each thread shows); 100 requests of one token 3.3, 3.0, 3.8 and 5.0.
+constexpr int kPlanPer = 2;
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -48,13 +51,25 @@ __device__ __forceinline__ int div_page(int n, uint64_t mul, int shift) {
   return (int)(((uint64_t)(uint32_t)n * mul) >> shift);
 }
 
+// The last of R entries of the ascending array `first` that is not above i.
+__device__ __forceinline__ int holder(const int* first, int R, int i) {
+  int lo = 0, hi = R;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanArgs a) {
-  // per request: cached length (complemented when released), first wanted or released page in
-  // the step's order, first token
+  // per request: cached length (complemented when released), and prefix sums over the requests of
+  // wanted pages, released pages and new tokens
   extern __shared__ int sm[];
   int* s_cached = sm;
-  int* s_first = sm + a.R;
-  int* s_cu = sm + 2 * a.R;  // R + 1
+  int* s_want = sm + a.R;
+  int* s_back = sm + 2 * a.R;    // R + 1
+  int* s_cu = sm + 3 * a.R + 1;  // R + 1
   __shared__ Sum3 warp_sum[32];
   __shared__ Sum3 carry;
   __shared__ int s_bits;
@@ -112,7 +127,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
     ex = ex + Sum3{x.want - v.want, x.grow - v.grow, x.back - v.back};
     if (b < a.R) {  // the low words are exact whenever the plan is accepted
       s_cached[b] = add < 0 ? ~cached : cached;
-      s_first[b] = (int)(add < 0 ? ex.back : ex.want);
+      s_want[b] = (int)ex.want;
+      s_back[b] = (int)ex.back;
       s_cu[b] = (int)ex.grow;
     }
     __syncthreads();
@@ -128,26 +144,26 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
   if (total.grow > a.max_tokens) bits |= FA_PLAN_TOO_MANY_TOKENS;
   const bool ok = bits == 0;
   const int tokens = ok ? (int)total.grow : 0;
-  if (tid == 0) s_cu[a.R] = tokens;
+  const int back = ok ? (int)total.back : 0;
+  if (tid == 0) s_cu[a.R] = tokens, s_back[a.R] = back;
   __syncthreads();
   const int gt = rank * nt + tid, gn = ctas * nt;
-  if (ok && total.back > 0) {  // released pages onto the stack, a warp per request
-    for (int b = rank * nw + warp; b < a.R; b += ctas * nw) {
-      const int c = s_cached[b];
-      if (c >= 0) continue;
-      const int used = pages_of(~c);
-      const int* row = a.table + (long long)b * a.table_stride;
-      int* top = a.free_pages + free0 + s_first[b];
-      for (int p0 = lane; p0 < used; p0 += 32 * kPlanBatch) {
-        int page[kPlanBatch];
+  // released pages onto the stack, kPlanPer neighbouring ones per thread
+  for (int p0 = gt * kPlanPer; p0 < back;) {
+    const int n = min(kPlanPer, back - p0);
+    int b = holder(s_back, a.R, p0), page[kPlanPer];
 #pragma unroll
-        for (int i = 0; i < kPlanBatch; ++i)
-          if (p0 + 32 * i < used) page[i] = row[p0 + 32 * i];
-#pragma unroll
-        for (int i = 0; i < kPlanBatch; ++i)
-          if (p0 + 32 * i < used) top[p0 + 32 * i] = page[i];
+    for (int i = 0; i < kPlanPer; ++i) {
+      if (i < n) {
+        while (s_back[b + 1] <= p0 + i) ++b;
+        page[i] = a.table[(long long)b * a.table_stride + (p0 + i - s_back[b])];
       }
     }
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i)
+      if (i < n) a.free_pages[free0 + p0 + i] = page[i];
+    if (back - p0 <= gn * kPlanPer) break;
+    p0 += gn * kPlanPer;
   }
   // Every block has read the inputs (nothing that may be one of them is written before), and the
   // released pages are on the stack.
@@ -164,20 +180,12 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
     a.cu_tokens[b] = ok ? s_cu[b] : 0;
   }
   const int top = (int)(avail - 1);
-  for (int t0 = gt * kPlanTokens; t0 < a.max_tokens; t0 += gn * kPlanTokens) {
-    int lo = 0;
-    if (t0 < tokens) {
-      int hi = a.R;  // the request with cu[lo] <= t0 < cu[lo + 1]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_cu[mid] <= t0) lo = mid;
-        else hi = mid;
-      }
-    }
-    int pos[kPlanTokens], req[kPlanTokens], page[kPlanTokens], in[kPlanTokens];
-    int* enter[kPlanTokens];
+  for (int t0 = gt * kPlanPer; t0 < a.max_tokens; t0 += gn * kPlanPer) {
+    int lo = t0 < tokens ? holder(s_cu, a.R, t0) : 0;
+    int pos[kPlanPer], req[kPlanPer], page[kPlanPer], in[kPlanPer];
+    int* enter[kPlanPer];
 #pragma unroll
-    for (int i = 0; i < kPlanTokens; ++i) {
+    for (int i = 0; i < kPlanPer; ++i) {
       const int t = t0 + i;
       pos[i] = 0, req[i] = -1, page[i] = -1, in[i] = 0, enter[i] = nullptr;
       if (t < tokens) {
@@ -189,22 +197,21 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
         in[i] = pos[i] - p * ps;
         int* entry = a.table + (long long)lo * a.table_stride + p;
         if (p >= used && in[i] == 0) enter[i] = entry;  // the first token of a page of this step
-        page[i] = p < used ? *entry : a.free_pages[top - (s_first[lo] + p - used)];
+        page[i] = p < used ? *entry : a.free_pages[top - (s_want[lo] + p - used)];
       }
     }
-    long long slot[kPlanTokens];
+    long long slot[kPlanPer];
 #pragma unroll
-    for (int i = 0; i < kPlanTokens; ++i) {
+    for (int i = 0; i < kPlanPer; ++i) {
       slot[i] = t0 + i < tokens ? (long long)page[i] * ps + in[i] : -1;
       if (enter[i]) *enter[i] = page[i];
     }
-    if (a.wide && t0 + kPlanTokens <= a.max_tokens) {
+    if (a.wide && t0 + kPlanPer <= a.max_tokens) {
       *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
-      *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
-      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      *reinterpret_cast<int4*>(a.token_req + t0) = make_int4(req[0], req[1], req[2], req[3]);
+      *reinterpret_cast<int2*>(a.positions + t0) = make_int2(pos[0], pos[1]);
+      *reinterpret_cast<int2*>(a.token_req + t0) = make_int2(req[0], req[1]);
     } else {
-      for (int i = 0; i < kPlanTokens && t0 + i < a.max_tokens; ++i)
+      for (int i = 0; i < kPlanPer && t0 + i < a.max_tokens; ++i)
         a.slots[t0 + i] = slot[i], a.positions[t0 + i] = pos[i], a.token_req[t0 + i] = req[i];
     }
   }
@@ -938,7 +945,7 @@ cudaError_t launch_paged_plan(PlanArgs a, cudaStream_t stream) {
   page_division(a.page_size, &a.page_mul, &a.page_shift);
   a.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions) |
              reinterpret_cast<uintptr_t>(a.token_req)) & 15) == 0;
-  const int smem = (3 * a.R + 1) * 4;
+  const int smem = (4 * a.R + 2) * 4;
   if (smem > 48 * 1024) {
     static bool attr_set[64];
     int dev = 0;
@@ -946,14 +953,15 @@ cudaError_t launch_paged_plan(PlanArgs a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
       e = cudaFuncSetAttribute(fa_paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (3 * FA_PLAN_MAX_REQUESTS + 1) * 4);
+                               (4 * FA_PLAN_MAX_REQUESTS + 2) * 4);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
   }
-  const long long share = (long long)kPlanThreads * kPlanTokens;
-  const int ctas = (int)std::min<long long>(kPlanMaxCtas, std::max<long long>(1, (a.max_tokens + share - 1) / share));
-  const int need = std::max(a.R, ctas > 1 ? kPlanThreads : (a.max_tokens + kPlanTokens - 1) / kPlanTokens);
+  const long long share = (long long)kPlanThreads * kPlanPer;
+  const int ctas = (int)std::min<long long>(
+      kPlanMaxCtas, std::max<long long>({1, (a.R + kPlanRequests - 1) / kPlanRequests, (a.max_tokens + share - 1) / share}));
+  const int need = std::max(a.R, ctas > 1 ? kPlanThreads : (a.max_tokens + kPlanPer - 1) / kPlanPer);
   const int threads = std::min(kPlanThreads, std::max(64, (need + 31) / 32 * 32));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);

@@ -37,7 +37,7 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_get_device_status",
 # Size of the library's built-in scratch used by fa_bwd_noalloc (include/fa.h).
 NOALLOC_MAX_SCRATCH_BYTES = 64 << 20
 # fa_paged_plan: most requests of a step and the bits of its status (include/fa.h).
-PLAN_MAX_REQUESTS = 16384
+PLAN_MAX_REQUESTS = 12288
 PAGED_MAX_LEN = 2**31 - 2**16  # most tokens of a row of the block table, and of a step
 PLAN_NO_PAGES, PLAN_ROW_FULL, PLAN_TOO_MANY_TOKENS, PLAN_BAD_INPUT = 1, 2, 4, 8
 
