@@ -343,6 +343,23 @@ def test_append_e4m3_saturates_and_keeps_nan(cuda_ok):
     assert torch.isnan(got[:, 2]).all()
 
 
+@pytest.mark.gpu
+def test_append_e4m3_rounds_the_quotient(cuda_ok):
+    # codes equal the cast of the fp32 quotient, on rounding borders too: every bf16 value from 2^-12 to
+    # 2^11, both signs, over factors that are powers of two, odd integers (exact ties among the
+    # quotients), reciprocals, tiny and huge
+    x = torch.arange(0x3980, 0x4500, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.cat([x, -x]).cuda()
+    T = x.numel() // 64
+    x = x[:T * 64].reshape(T, 1, 64)
+    for f in (0.25, 1.0, 3.0, 5.0, 7.0, 0.1, 1 / 3, 0.7, 0.0123, 448.0 / 3, 2.0 ** -120, 1e-38, 1e-40, 3e35):
+        kc, vc = torch.zeros(2, T, 1, 1, 64, device="cuda", dtype=torch.float8_e4m3fn)
+        d = torch.tensor([f], device="cuda")
+        fa.paged_append(x, x, x, None, None, None, None, torch.arange(T, device="cuda"), kc, vc, v_descale=d)
+        want = (x.float() / d).clamp(-448, 448).to(torch.float8_e4m3fn)
+        assert torch.equal(vc[:, 0].view(torch.uint8), want.view(torch.uint8)), f
+
+
 # ------------------------------------------------------------------ decode on the GPU
 def _pool(lens, ps, Hk, d, fp8, seed, cols=None, poison=True):
     """Caches whose unused slots and pages are NaN, block table with -1 past a row's pages, and fp64
