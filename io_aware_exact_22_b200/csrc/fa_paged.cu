@@ -242,8 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
 // and a low part, so the product's rounding stays below the output's), with an E4M3 cache, whose
 // values are exact in fp16, as one fp16 term.
 constexpr int kWarps = 4;
-constexpr int kStages = 2;
-constexpr int kCtasPerSm = 3;
+constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxRows = 16;
 
 template <int D, bool FP8>
@@ -253,8 +252,13 @@ struct DecCfg {
   static constexpr int KEYS = ROWB == 256 ? 16 : 32;      // keys per warp and tile
   static constexpr int STAGE = 2 * KEYS * ROWB;           // K then V
   static constexpr int RPI = 32 / CH;                     // rows that one copy instruction covers
+  // More warps for bf16, more registers and bytes in flight per warp for E4M3, whose conversions are
+  // the longer chain: 3 CTAs of 2 stages against 2 of 3 take 51.7 and 53.5 us for 32 rows of 0-4096
+  // keys in bf16, 116.5 and 111.5 us for 64 rows of 1024-8192 keys in E4M3.
+  static constexpr int STAGES = FP8 ? 3 : 2;
+  static constexpr int CTAS = FP8 && D == 128 ? 2 : kMaxCtasPerSm;
   static constexpr int RS = D + 4;                        // floats of a row of O at the join: off one bank
-  static constexpr int SMEM = kWarps * kStages * STAGE;
+  static constexpr int SMEM = kWarps * STAGES * STAGE;
   static_assert(8 * RS * 4 <= STAGE, "a stage holds 8 rows of a warp's O at the join");
 };
 
@@ -266,7 +270,7 @@ __device__ __forceinline__ int swz(int r) {
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -402,9 +406,10 @@ constexpr float kSlack = 8.f;
 constexpr float kPBias = 7.f;
 
 template <int D, bool FP8, int NQ>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_decode_kernel(const DecodeArgs a) {
   using C = DecCfg<D, FP8>;
   constexpr int KEYS = C::KEYS, MT = KEYS / 16, CH = C::CH, ROWB = C::ROWB;
+  constexpr int kStages = C::STAGES;
   constexpr int DC = D / 16;  // 16-wide steps of the score product, and 16-row tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_scan[kWarps];
@@ -445,18 +450,20 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
   const long long ctas = min((long long)G, total);
   Part part = part_of(a.workspace, G);
 
-  // rows without a visible key
-  for (int t = cta; t < a.T; t += G) {
-    int r;
-    const int n = row_keys(a, t, r);
-    if (n > 0) continue;
-    if (n == 0)
-      for (int i = tid; i < a.Hq * (D / 4); i += kWarps * 32)
-        write_out<D>(a, t, i / (D / 4), i % (D / 4), make_float4(0, 0, 0, 0), 0.f, 0.f, 0.f, 0.f);
-    if (by_group)
-      for (int i = tid; i < groups; i += kWarps * 32) part.head[t * groups + i] = make_int4(-1, 0, 0, 0);
-  }
+  auto write_empty = [&]() {  // rows without a visible key
+    for (int t = cta; t < a.T; t += G) {
+      int r;
+      const int n = row_keys(a, t, r);
+      if (n > 0) continue;
+      if (n == 0)
+        for (int i = tid; i < a.Hq * (D / 4); i += kWarps * 32)
+          write_out<D>(a, t, i / (D / 4), i % (D / 4), make_float4(0, 0, 0, 0), 0.f, 0.f, 0.f, 0.f);
+      if (by_group)
+        for (int i = tid; i < groups; i += kWarps * 32) part.head[t * groups + i] = make_int4(-1, 0, 0, 0);
+    }
+  };
   if (cta >= ctas) {
+    write_empty();
     if (!by_group && tid == 0) part.head[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
@@ -535,6 +542,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) fa_paged_decode_kerne
     line[s] = ahead;
     fetch(s);
   }
+
+  write_empty();
 
   // ---- computing.  The thread's share of S^T and O^T: query rows 8 n + 2 i4 + e of keys (or
   // columns) g8 and g8 + 8 of each 16.
@@ -897,12 +906,12 @@ int sm_count() {
   return v;
 }
 
-int decode_ctas() { return kCtasPerSm * sm_count(); }
+int decode_ctas(int per_sm) { return per_sm * sm_count(); }
 
 template <int D, bool FP8, int NQ>
 cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t stream) {
   using C = DecCfg<D, FP8>;
-  static_assert(kCtasPerSm * (C::SMEM + 2048) <= 228 * 1024, "kCtasPerSm CTAs fit an SM");
+  static_assert(C::CTAS * (C::SMEM + 2048) <= 228 * 1024, "CTAS CTAs fit an SM");
   static bool attr_set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -912,7 +921,7 @@ cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev] = true;
   }
-  const int ctas = decode_ctas();
+  const int ctas = decode_ctas(C::CTAS);
   fa_paged_decode_kernel<D, FP8, NQ><<<ctas, kWarps * 32, C::SMEM, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // a block for every group that can be divided, and, when they are few, several for each
@@ -978,7 +987,7 @@ cudaError_t launch_paged_plan(PlanArgs a, cudaStream_t stream) {
 
 size_t paged_decode_workspace(int T, int Hq, int Hk, int d) {
   (void)T, (void)Hq, (void)Hk, (void)d;
-  const int ctas = decode_ctas();
+  const int ctas = decode_ctas(kMaxCtasPerSm);
   // hp * row bytes is at most 256, i.e. hp * d * 4 at most 1024 bytes (E4M3)
   return part_head_bytes(ctas) + part_ml_bytes(ctas) + (size_t)ctas * 2 * kMaxRows * 1024;
 }
