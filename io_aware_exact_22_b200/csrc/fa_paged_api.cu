@@ -214,7 +214,8 @@ fa_status_t fa_paged_decode(const void* q, const void* k_cache, const void* v_ca
                             long long c_st, long long c_sh, float scale, void* stream) {
   if (T < 0 || Hq < 0 || Hk < 0 || table_rows < 0 || table_cols < 0) return FA_ERR_INVALID_ARG;
   if (cache_fp8 != 0 && cache_fp8 != 1) return FA_ERR_INVALID_ARG;
-  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  if (!(std::isfinite(scale_log2) && scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (T == 0 || Hq == 0) return FA_OK;
   if (Hk == 0 || Hq % Hk != 0 || Hq > (1 << 20) || (double)T * Hq * d >= 4.6e18) return FA_ERR_INVALID_ARG;
@@ -243,7 +244,7 @@ fa_status_t fa_paged_decode(const void* q, const void* k_cache, const void* v_ca
   a.q_st = q_st, a.q_sh = q_sh;
   a.c_sp = c_sp * size, a.c_st = c_st * size, a.c_sh = c_sh * size;
   a.num_pages = num_pages, a.page_size = page_size, a.T = T, a.Hq = Hq, a.Hk = Hk;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  a.scale_log2 = scale_log2;
   return launch_paged_decode(d, cache_fp8 != 0, a, (cudaStream_t)stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

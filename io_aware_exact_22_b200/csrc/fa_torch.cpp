@@ -13,7 +13,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
+#include <cmath>
 #include <vector>
 
 #include "fa.h"
@@ -316,6 +318,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     "k and v must be [T,Hk,d] with the cache's Hk and q's T and d");
   distinct(c.k, "k_cache");
   distinct(c.v, "v_cache");
+  TORCH_CHECK_VALUE(c.k.numel() == 0 || c.k.data_ptr() != c.v.data_ptr(), "k_cache and v_cache must not be one tensor");
   const void* wq = vec_or_null(a[3], "wq", at::kBFloat16, index, d);
   const void* wk = vec_or_null(a[4], "wk", at::kBFloat16, index, d);
   const Rope r = rope_of(a[5], index);
@@ -346,7 +349,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(c.d == d && c.Hk > 0 && Hq % c.Hk == 0, "q's heads must be a multiple of the cache's, with its d");
   const Table t = table_of(a[3], index);
   const int* lens = static_cast<const int*>(vec(a[4], "lens", at::kInt, index, T));
-  const float scale = number(a[5]);
+  const float scale = a[5] == Py_None ? static_cast<float>(1.0 / std::sqrt(std::max(d, 1))) : number(a[5]);
   const int* req = static_cast<const int*>(vec_or_null(a[6], "req", at::kInt, index, T));
   const float *kd = c.descale(a[7], "k_descale", index), *vd = c.descale(a[8], "v_descale", index);
   const Tensor out = output(a[9], "out", at::kBFloat16, index, {T, Hq, d});

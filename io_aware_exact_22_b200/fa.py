@@ -512,9 +512,8 @@ def paged_append(q, k, v, wq, wk, rope, positions, slots, k_cache, v_cache, eps:
 
 def paged_decode(q, k_cache, v_cache, block_table, lens, scale: float | None = None, req=None, k_descale=None,
                  v_descale=None, out=None, lse=None, workspace=None):
-    """O [T,Hq,d] (bf16), LSE [T,Hq] of one query token per row, q [T,Hq,d], over the paged cache: row
-    t sees lens[t] keys (int32, on the device) of row req[t] of the block table (int32; None: of
+    """O [T,Hq,d] (bf16), LSE [T,Hq] of one query token per row, q [T,Hq,d], over the paged cache (scale: 1/sqrt(d)
+    if None): row t sees lens[t] keys (int32, on the device) of row req[t] of the block table (int32; None: of
     row t; negative: the output row stays as it was).  A row with no key gets O = 0, LSE = -inf."""
-    return _result((_ext or _load_ext()).paged_decode(q, k_cache, v_cache, block_table, lens,
-                                                      q.shape[-1] ** -0.5 if scale is None else scale, req, k_descale,
+    return _result((_ext or _load_ext()).paged_decode(q, k_cache, v_cache, block_table, lens, scale, req, k_descale,
                                                       v_descale, out, lse, workspace), "fa_paged_decode")

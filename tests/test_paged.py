@@ -248,6 +248,44 @@ def test_plan_in_place_over_many_steps_captured(cuda_ok):
         assert sorted(flat) == list(range(220))  # every page is in one place
 
 
+@pytest.mark.gpu
+def test_plan_on_a_whole_cluster_captured_and_on_a_side_stream(cuda_ok):
+    # 3000 requests are 8 blocks: one captured step, replayed from the same start, and the call on another stream
+    R, ps = 3000, 16
+    rng = np.random.default_rng(8)
+    cached, new = rng.integers(0, 200, R).tolist(), rng.integers(-1, 9, R).tolist()
+    table, free = _state(cached, ps, 14, 2000, 4)
+    most = sum(max(n, 0) for n in new) + 5
+    want = ref.plan(cached, new, table, free, ps, 14, most)
+    assert want["status"] == 0
+    t0, f0 = _ints(table), _ints(free + [-7] * 45000)
+    t, f, c, n, count = t0.clone(), f0.clone(), _ints(cached), _ints(new), _ints([len(free)])
+    o = {k: torch.full((m,), -99, dtype=torch.int64 if k == "slots" else torch.int32, device="cuda")
+         for k, m in (("lens", R), ("cu", R + 1), ("slots", most), ("positions", most), ("req", most), ("fco", 1), ("st", 1))}
+    step = lambda: fa.paged_plan(c, n, t, f, count, ps, o["lens"], o["cu"], o["slots"], o["positions"], o["req"],  # noqa: E731
+                                 o["fco"], o["st"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for replay in range(3):  # the side stream's result first, then the replays'
+        if replay:
+            t.copy_(t0)
+            f.copy_(f0)
+            graph.replay()
+        torch.cuda.synchronize()
+        assert o["st"].item() == 0 and t.tolist() == want["table"]
+        for k in ("lens", "cu", "slots", "positions", "req"):
+            assert o[k].tolist() == want[k], k
+            o[k].fill_(-99)
+        m = o["fco"].item()
+        assert m == len(want["free"]) and f[:m].tolist() == want["free"]
+
+
 # ------------------------------------------------------------------ append on the GPU
 def _e4m3(x):
     return torch.from_numpy(oracle.e4m3_decode(x.view(torch.uint8).cpu().numpy()))
@@ -599,6 +637,13 @@ def test_binding_refuses(cuda_ok):
             call()
     with pytest.raises(fa.FAError):
         fa.paged_decode(q, kc, vc, t, n, scale=-1.0)
+    with pytest.raises(ValueError):
+        fa.paged_decode(q[:, :, :0], kc, vc, t, n)
+    x = q[:, :2]
+    with pytest.raises(ValueError):
+        fa.paged_append(q, x, x, None, None, None, None, n.long(), kc, kc)
+    with pytest.raises(TypeError):
+        fa.paged_decode(q, kc, vc, t, [40])
     with pytest.raises(fa.FAError):
         fa.paged_decode(q, kc, vc, torch.empty(0, 3, dtype=torch.int32, device="cuda"), n)
 
