@@ -64,13 +64,43 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// Arithmetic on a lane's chunks goes two elements an instruction (fp32 pairs).
+__device__ __forceinline__ uint64_t pair(const float (&x)[8], int i) { return f2_pack(x[2 * i], x[2 * i + 1]); }
+__device__ __forceinline__ void set_pair(float (&x)[8], int i, uint64_t v) { f2_unpack(v, x[2 * i], x[2 * i + 1]); }
+// x *= y f
+__device__ __forceinline__ void scale8(float (&x)[8], const float (&y)[8], float f) {
+  const uint64_t ff = f2_pack(f, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) set_pair(x, i, f2_mul(pair(x, i), f2_mul(pair(y, i), ff)));
+}
+__device__ __forceinline__ void scale8(float (&x)[8], float f) {
+  const uint64_t ff = f2_pack(f, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) set_pair(x, i, f2_mul(pair(x, i), ff));
+}
+__device__ __forceinline__ void mul8(float (&x)[8], const float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) set_pair(x, i, f2_mul(pair(x, i), pair(y, i)));
+}
+// acc + sum of x y, the even elements' and the odd ones' apart
+__device__ __forceinline__ uint64_t dot8(const float (&x)[8], const float (&y)[8], uint64_t acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc = f2_fma(pair(x, i), pair(y, i), acc);
+  return acc;
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a + b;
+}
+
 // One lane's share of a token's rotation: its chunks a and b (8 elements each), whether they are
 // rotated, and the angles.  Halves: pair e is (a_e, b_e) with c[e], s[e]; both chunks are rotated or
 // neither is.  Interleaved: pair i < 4 is (a_2i, a_2i+1) with c[i], s[i], and b's have c[4 + i], s[4 + i].
 template <int D, bool INTER>
 struct Rotation {
   static constexpr int LPR = D / 16;
-  float c[8], s[8];
+  float c[8], s[8], ns[8];  // ns = -s
   int ca, cb;
   bool on_a, on_b;
 
@@ -104,7 +134,16 @@ struct Rotation {
       if (on_b) inside<BACK>(b, 4);
     } else if (on_a) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) turn<BACK>(a[e], b[e], e);
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t x = pair(a, i), y = pair(b, i);
+        if (BACK) {  // (the backward has no registers for ns)
+          set_pair(a, i, f2_fma(x, pair(c, i), f2_mul(y, pair(s, i))));
+          set_pair(b, i, f2_fma(f2_mul(x, pair(s, i)), f2_pack(-1.f, -1.f), f2_mul(y, pair(c, i))));
+        } else {
+          set_pair(a, i, f2_fma(x, pair(c, i), f2_mul(y, pair(ns, i))));
+          set_pair(b, i, f2_fma(y, pair(c, i), f2_mul(x, pair(s, i))));
+        }
+      }
     }
   }
 
@@ -113,17 +152,17 @@ struct Rotation {
     const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p + half));
     c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
     s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-  }
-  template <bool BACK>
-  __device__ __forceinline__ void turn(float& a, float& b, int e) const {
-    const float x = a, y = b, sn = BACK ? -s[e] : s[e];
-    a = x * c[e] - y * sn;
-    b = y * c[e] + x * sn;
+#pragma unroll
+    for (int e = i; e < i + 4; ++e) ns[e] = -s[e];
   }
   template <bool BACK>
   __device__ __forceinline__ void inside(float (&x)[8], int i0) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) turn<BACK>(x[2 * i], x[2 * i + 1], i0 + i);
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i], b = x[2 * i + 1], sn = BACK ? -s[i0 + i] : s[i0 + i];
+      x[2 * i] = a * c[i0 + i] - b * sn;
+      x[2 * i + 1] = b * c[i0 + i] + a * sn;
+    }
   }
 };
 
@@ -155,10 +194,7 @@ __device__ __forceinline__ Raw ld_weight(const __nv_bfloat16* w, int ca, int cb)
 // 1 / sqrt(mean of the row's squares + eps)
 template <int D>
 __device__ __forceinline__ float inv_rms(const float (&a)[8], const float (&b)[8], float eps) {
-  float ss = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
-  return rsqrtf(row_sum<D / 16>(ss) * (1.f / D) + eps);
+  return rsqrtf(row_sum<D / 16>(sum2(dot8(b, b, dot8(a, a, 0)))) * (1.f / D) + eps);
 }
 __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8]) {
   return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
@@ -264,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const NormRop
       slot_i = slot_i == kDepth - 1 ? 0 : slot_i + 1;
       if (MODE == kTrain || kind < 2) {
         const float r = inv_rms<D>(ya, yb, a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ya[e] *= r * wa[e], yb[e] *= r * wb[e];
+        scale8(ya, wa, r);
+        scale8(yb, wb, r);
         t.template apply<false>(ya, yb);
       }
       if (!go) continue;
@@ -386,19 +422,23 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const Nor
       float wa[8], wb[8];
       unpack8(w.a, wa);
       unpack8(w.b, wb);
-      float dot = 0.f;
+      scale8(xa, r);
+      scale8(xb, r);
+      if (go) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xa[e] *= r, xb[e] *= r;
-        if (go) dwa[e] = fmaf(ga[e], xa[e], dwa[e]), dwb[e] = fmaf(gb[e], xb[e], dwb[e]);
-        ga[e] *= wa[e], gb[e] *= wb[e];
-        dot = fmaf(ga[e], xa[e], fmaf(gb[e], xb[e], dot));
+        for (int i = 0; i < 4; ++i) {
+          set_pair(dwa, i, f2_fma(pair(ga, i), pair(xa, i), pair(dwa, i)));
+          set_pair(dwb, i, f2_fma(pair(gb, i), pair(xb, i), pair(dwb, i)));
+        }
       }
-      const float c = row_sum<LPR>(dot) * (1.f / D);
+      mul8(ga, wa);
+      mul8(gb, wb);
+      const float c = row_sum<LPR>(sum2(dot8(gb, xb, dot8(ga, xa, 0)))) * (1.f / D);
+      const uint64_t rr = f2_pack(r, r), nc = f2_pack(-c, -c);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ga[e] = r * (ga[e] - xa[e] * c);
-        gb[e] = r * (gb[e] - xb[e] * c);
+      for (int i = 0; i < 4; ++i) {
+        set_pair(ga, i, f2_mul(rr, f2_fma(pair(xa, i), nc, pair(ga, i))));
+        set_pair(gb, i, f2_mul(rr, f2_fma(pair(xb, i), nc, pair(gb, i))));
       }
       if (go) st_row(dst, t.ca, t.cb, pack8(ga), pack8(gb));
       dst += dx_sh;
