@@ -250,7 +250,7 @@ def test_plan_in_place_over_many_steps_captured(cuda_ok):
 
 @pytest.mark.gpu
 def test_plan_on_a_whole_cluster_captured_and_on_a_side_stream(cuda_ok):
-    # 3000 requests are 8 blocks: one captured step, replayed from the same start, and the call on another stream
+    # 3000 requests are a full cluster: one captured step, replayed from the same start, and the call on another stream
     R, ps = 3000, 16
     rng = np.random.default_rng(8)
     cached, new = rng.integers(0, 200, R).tolist(), rng.integers(-1, 9, R).tolist()
