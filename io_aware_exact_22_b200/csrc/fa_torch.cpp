@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -86,15 +87,32 @@ Tensor output(PyObject* o, const char* name, at::ScalarType type, int index, at:
   return t;
 }
 
-Tensor workspace(PyObject* o, size_t bytes, int index) {
-  if (o == Py_None)
-    return at::empty({static_cast<int64_t>(std::max<size_t>(bytes, 256))},
-                     at::TensorOptions().dtype(at::kByte).device(at::kCUDA, index));
-  const Tensor& t = tensor(o, "workspace");
-  TORCH_CHECK_VALUE(t.scalar_type() == at::kByte && on(t, index) && t.is_contiguous() && (size_t)t.numel() >= bytes,
-                    "workspace must be a contiguous uint8 tensor of at least ", bytes, " bytes on CUDA device ", index);
-  return t;
-}
+// The caller's workspace, checked, or one from torch's allocator that goes back to it when the call
+// returns (it is handed out again in the order of the current stream).  The device is current.
+class Workspace {
+ public:
+  Workspace(PyObject* o, size_t bytes, int index) : bytes_(std::max<size_t>(bytes, 256)) {
+    if (o == Py_None) {
+      at_ = own_ = c10::cuda::CUDACachingAllocator::raw_alloc(bytes_);
+      return;
+    }
+    const Tensor& t = tensor(o, "workspace");
+    TORCH_CHECK_VALUE(t.scalar_type() == at::kByte && on(t, index) && t.is_contiguous() && (size_t)t.numel() >= bytes,
+                      "workspace must be a contiguous uint8 tensor of at least ", bytes, " bytes on CUDA device ", index);
+    at_ = t.data_ptr(), bytes_ = t.numel();
+  }
+  ~Workspace() {
+    if (own_) c10::cuda::CUDACachingAllocator::raw_delete(own_);
+  }
+  Workspace(const Workspace&) = delete;
+  Workspace& operator=(const Workspace&) = delete;
+  void* at() const { return at_; }
+  size_t bytes() const { return bytes_; }
+
+ private:
+  void *at_ = nullptr, *own_ = nullptr;
+  size_t bytes_;
+};
 
 // An output's elements lie at addresses of their own: each stride is past all that the smaller ones reach.
 void distinct(const Tensor& t, const char* name) {
@@ -268,11 +286,12 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor dq = gradient(a[10], "dq", x.q), dk = gradient(a[11], "dk", x.k);
   const auto f32 = at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, x.index);
   const Tensor dwq = at::empty({x.d}, f32), dwk = at::empty({x.d}, f32);
-  const Tensor ws = workspace(a[12], c_norm_rope_bwd_bytes(x.B, x.N, x.Hq, x.Hk, x.d), x.index);
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
+  const Workspace ws(a[12], c_norm_rope_bwd_bytes(x.B, x.N, x.Hq, x.Hk, x.d), x.index);
   const fa_status_t st = launch(x.index, [&](void* stream) {
     return c_norm_rope_bwd(gqp, gkp, x.q.data_ptr(), x.k.data_ptr(), wq, wk, r.table, r.rows, r.rot, inter, p.at, p.stride,
                            dq.data_ptr(), dk.data_ptr(), static_cast<float*>(dwq.data_ptr()),
-                           static_cast<float*>(dwk.data_ptr()), ws.data_ptr(), ws.numel(), x.B, x.N, x.Hq, x.Hk, x.d,
+                           static_cast<float*>(dwk.data_ptr()), ws.at(), ws.bytes(), x.B, x.N, x.Hq, x.Hk, x.d,
                            x.q.stride(0), x.q.stride(1), x.q.stride(2), x.k.stride(0), x.k.stride(1), x.k.stride(2),
                            dq.stride(0), dq.stride(1), dq.stride(2), dk.stride(0), dk.stride(1), dk.stride(2), eps, stream);
   });
@@ -354,15 +373,11 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float *kd = c.descale(a[7], "k_descale", index), *vd = c.descale(a[8], "v_descale", index);
   const Tensor out = output(a[9], "out", at::kBFloat16, index, {T, Hq, d});
   const Tensor lse = output(a[10], "lse", at::kFloat, index, {T, Hq});
-  size_t bytes;
-  {
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
-    bytes = c_decode_bytes(T, Hq, c.Hk, d);
-  }
-  const Tensor ws = workspace(a[11], bytes, index);
+  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+  const Workspace ws(a[11], c_decode_bytes(T, Hq, c.Hk, d), index);
   const fa_status_t st = launch(index, [&](void* stream) {
     return c_decode(q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.fp8, kd, vd, t.at, t.stride, t.rows, t.cols, lens, req,
-                    out.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.data_ptr(), ws.numel(), c.pages, c.page_size, T,
+                    out.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.at(), ws.bytes(), c.pages, c.page_size, T,
                     Hq, c.Hk, d, q.stride(0), q.stride(1), c.k.stride(0), c.k.stride(1), c.k.stride(2), scale, stream);
   });
   return st ? PyLong_FromLong(st) : tensors(out, lse);
