@@ -356,6 +356,11 @@ struct Cursor {
   int t, hm, tile, tiles, len, r;
 };
 
+// a / b for a >= 0, b > 0, by the short division when both fit 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 __device__ __forceinline__ int tiles_of(int len, int shift) { return (max(len, 0) + (1 << shift) - 1) >> shift; }
 
 __device__ __forceinline__ void cursor_next(const DecodeArgs& a, Cursor& c, int groups, int shift) {
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
   constexpr int DC = D / 16;  // 16-wide steps of the score product, and 16-row tiles of O^T
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_scan[kWarps];
-  __shared__ int s_start[3];
+  __shared__ Cursor s_start;
   __shared__ float s_m[kWarps][kMaxRows], s_l[kWarps][kMaxRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = gridDim.x, cta = blockIdx.x;
@@ -436,9 +441,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
   const int per_thread = (a.T + kWarps * 32 - 1) / (kWarps * 32);
   const int t0 = min(a.T, tid * per_thread), t1 = min(a.T, t0 + per_thread);
   long long mine = 0;
+  int len = 0, r = 0;  // of the thread's last row: its only one, as a rule
   for (int t = t0; t < t1; ++t) {
-    int r;
-    mine += tiles_of(row_keys(a, t, r), shift);
+    len = row_keys(a, t, r);
+    mine += tiles_of(len, shift);
   }
   long long x = mine;
 #pragma unroll
@@ -476,29 +482,24 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
     if (!by_group && tid == 0) part.head[cta] = make_int4(-1, 0, 0, 0);
     return;
   }
-  const long long first = total * cta / ctas, last = total * (cta + 1) / ctas;  // [first, last)
+  // CTA c's run begins at tile c * per + min(c, extra) and has per tiles, one more below extra
+  const long long per = quotient(total, ctas), extra = total - per * ctas, first = cta * per + min((long long)cta, extra);
   if (before * groups <= first && first < (before + mine) * groups) {
     long long at = before * groups;
     for (int t = t0; t < t1; ++t) {
-      int r;
-      const long long n = tiles_of(row_keys(a, t, r), shift);
+      if (t1 - t0 > 1) len = row_keys(a, t, r);
+      const long long n = tiles_of(len, shift);
       if (first < at + n * groups) {
-        s_start[0] = t;
-        s_start[1] = (int)((first - at) / n);
-        s_start[2] = (int)((first - at) % n);
+        const long long hm = quotient(first - at, n);
+        s_start = {t, (int)hm, (int)(first - at - hm * n), (int)n, len, r};
         break;
       }
       at += n * groups;
     }
   }
   __syncthreads();
-  Cursor ahead;  // the next tile to fetch
-  ahead.t = s_start[0];
-  ahead.hm = s_start[1];
-  ahead.tile = s_start[2];
-  ahead.len = row_keys(a, ahead.t, ahead.r);
-  ahead.tiles = tiles_of(ahead.len, shift);
-  int fetch_left = (int)(last - first);
+  Cursor ahead = s_start;  // the next tile to fetch
+  int fetch_left = (int)(per + (cta < extra));
   int left = fetch_left;
 
   // ---- fetching.  One copy instruction covers RPI keys.  A page size that is a multiple of RPI
@@ -760,9 +761,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
       const bool whole = seg_end && seg_tile0 == 0;
       const int slot = 2 * cta + (seg_tile0 == 0 ? 1 : 0);
       if (tid == 0 && seg_tile0 == 0 && (by_group || left == 0)) {  // the group began here: is it divided?
-        const long long end = last - 1 + (cur.tiles - 1 - cur.tile);  // its last tile, if it is
+        // the CTA that holds its last tile, if it is (its present tile is then the last of this CTA's run)
+        const long long end = first + per + (cta < extra) - 1 + (cur.tiles - 1 - cur.tile), split = extra * (per + 1);
+        const long long holder = end < split ? quotient(end, per + 1) : extra + quotient(end - split, per);
         part.head[by_group ? cur.t * groups + cur.hm : cta] =
-            whole ? make_int4(-1, 0, 0, 0) : make_int4(cur.t, cur.hm, cta, (int)(((end + 1) * ctas - 1) / total));
+            whole ? make_int4(-1, 0, 0, 0) : make_int4(cur.t, cur.hm, cta, (int)holder);
       }
       __syncwarp();
 #pragma unroll
