@@ -216,13 +216,13 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const NormRop
   __shared__ __align__(16) uint8_t ring[kThreads / 32 * kDepth * 1024];
   const int lane = threadIdx.x & 31, j = lane % LPR;
   const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long run = unit / a.chunks;
+  const long long run = quotient(unit, a.chunks);
   const long long tok = run * G + lane / LPR;
   const int h0 = (int)(unit - run * a.chunks) * a.heads_per_unit;
   const int heads = a.Hq + a.Hk * (MODE == kTrain ? 1 : 2);
   const int h1 = min(heads, h0 + a.heads_per_unit);
   const bool live = tok < (long long)a.B * a.N;
-  const int b = live ? (int)(tok / a.N) : 0, n = live ? (int)(tok - (long long)b * a.N) : 0;
+  const int b = MODE == kTrain && live ? (int)quotient(tok, a.N) : 0, n = live ? (int)(tok - (long long)b * a.N) : 0;
   Rotation<D, INTER> t(a.rot, j);
 
   // What the token needs; `go`: it is computed.
@@ -261,18 +261,18 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const NormRop
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) fetch(i);
 
-  long long cache_off = 0;
-  bool bad = a.rot > 0 && (pos < 0 || pos >= a.rope_rows);
-  if (MODE != kTrain) {
-    bad |= slot >= (long long)a.num_pages * a.page_size;
-    const long long page = slot / a.page_size;
-    cache_off = page * a.c_sp + (slot - page * a.page_size) * a.c_st;
-  }
+  const bool bad = (a.rot > 0 && (pos < 0 || pos >= a.rope_rows)) ||
+                   (MODE != kTrain && slot >= (long long)a.num_pages * a.page_size);
   if (go && bad) {
     if (j == 0) atomicOr(a.status, FA_DEV_BOUNDS);
     go = false;
   }
   if (go) t.load(a.rope, a.rot, pos);
+  long long cache_off = 0;
+  if (MODE != kTrain && go) {
+    const long long page = quotient(slot, a.page_size);
+    cache_off = page * a.c_sp + (slot - page * a.page_size) * a.c_st;
+  }
   int slot_i = 0;
   for (int hh = h0; hh < h1;) {
     const int kind = kind_of(hh), end = end_of(kind);
@@ -365,12 +365,12 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const Nor
     int h, h1, b, n;
   };
   auto enter = [&](Place& p) {  // the first head of p.unit
-    const long long run = p.unit / chunks;
+    const long long run = quotient(p.unit, chunks);
     p.tok = run * G + lane / LPR;
     p.h = (int)(p.unit - run * chunks) * a.heads_per_unit;
     p.h1 = min(H, p.h + a.heads_per_unit);
     if (p.tok < tokens) {
-      p.b = (int)(p.tok / a.N), p.n = (int)(p.tok - (long long)p.b * a.N);
+      p.b = (int)quotient(p.tok, a.N), p.n = (int)(p.tok - (long long)p.b * a.N);
       p.x = xs + p.b * (is_q ? a.q_sb : a.k_sb) + p.n * (is_q ? a.q_sn : a.k_sn) + p.h * x_sh;
       p.g = gs + (((long long)p.b * H + p.h) * a.N + p.n) * D;
     }
@@ -398,11 +398,11 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const Nor
 
   int slot_i = 0;
   for (long long unit = (long long)block * W + warp; unit < units; unit += (long long)blocks * W) {
-    const long long run = unit / chunks;
+    const long long run = quotient(unit, chunks);
     const long long tok = run * G + lane / LPR;
     const int h0 = (int)(unit - run * chunks) * a.heads_per_unit, h1 = min(H, h0 + a.heads_per_unit);
     bool go = tok < tokens;
-    const int b = go ? (int)(tok / a.N) : 0, n = go ? (int)(tok - (long long)b * a.N) : 0;
+    const int b = go ? (int)quotient(tok, a.N) : 0, n = go ? (int)(tok - (long long)b * a.N) : 0;
     int pos = n;
     if (a.rot > 0 && a.positions && go) pos = a.positions[(long long)b * a.pos_sb + n];
     if (go && a.rot > 0 && (pos < 0 || pos >= a.rope_rows)) {

@@ -356,11 +356,6 @@ struct Cursor {
   int t, hm, tile, tiles, len, r;
 };
 
-// a / b for a >= 0, b > 0, by the short division when both fit 32 bits.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 __device__ __forceinline__ int tiles_of(int len, int shift) { return (max(len, 0) + (1 << shift) - 1) >> shift; }
 
 __device__ __forceinline__ void cursor_next(const DecodeArgs& a, Cursor& c, int groups, int shift) {
