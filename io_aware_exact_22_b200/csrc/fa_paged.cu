@@ -17,7 +17,7 @@ using namespace ptx;
 // Requests hold cached[b] tokens in ceil(cached[b] / page_size) pages; the step adds
 // new_tokens[b] tokens, or releases the request (-1).  Released pages go on top of the free stack
 // in the order (request, page), wanted pages come off its top in the same order, so the result
-// depends on the inputs alone.  Bound by latency: 3.6 us for 16 decoding requests, 9.3 us for 1000
+// depends on the inputs alone.  Bound by latency: 3.2 us for 16 decoding requests, 9.8 us for 1000
 // mixed ones with 50 k tokens.  Everything is one kernel: every block of one cluster scans the
 // requests for itself (a few bytes each, from L2), the cluster's barrier separates reading the
 // inputs from writing, which is what lets the outputs alias them, and then the tokens are spread
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
 //
 // Bound by HBM once contexts are long; about 8 us go to the launches, to the chain of lengths, pages
 // and keys, and to the join.  On a B200, replayed from a graph: 2 x 131071 keys, 32 query and 4 kv heads,
-// d=128, bf16 95 us (5.6 TB/s), 32 rows of 0 to 4096 keys, 32 and 8 heads 51.6 us (5.2 TB/s), 64 rows of
-// 1024 to 8192 keys, 64 and 8 heads, E4M3 108 us (5.6 TB/s), one row of 300 keys 8.4 us.  (With the
+// d=128, bf16 93 us (5.8 TB/s), 32 rows of 0 to 4096 keys, 32 and 8 heads 50.7 us (5.3 TB/s), 64 rows of
+// 1024 to 8192 keys, 64 and 8 heads, E4M3 107 us (5.7 TB/s), one row of 300 keys 7.9 us.  (With the
 // queries on the 16-row side, 2 CTAs of 3 stages and a serial join: 105, 56, 137 and 8.0 us.)
 constexpr int kWarps = 4;
 constexpr int kMaxCtasPerSm = 3;
