@@ -22,8 +22,8 @@
 // Bound by HBM.  On a B200, replayed from a graph: B=1 N=16384, 64 heads, d=128 takes 87 us (6.2 TB/s,
 // 0.95 of a copy; rows loaded to registers, two to four ahead, took 115 to 148), its gradient at B=2
 // N=4096, 32 heads 38.5 us (5.3 TB/s, of which 2 us add up the weights' gradients), the cache form
-// with 4099 tokens of 40 heads to E4M3 18 us (4.5 TB/s: one wave of warps, whose slots, positions and table rows
-// come one after the other), 8 tokens 3.1 us.
+// with 4099 tokens of 40 heads to E4M3 16 us (5.1 TB/s, from L2 in part: one wave of warps, whose slots,
+// positions and table rows come one after the other), 8 tokens 3.0 us.
 #include "fa_internal.cuh"
 #include "sm100_ptx.cuh"
 
@@ -206,6 +206,32 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8]) {
   return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
+// a, b over f, such that the rounding to E4M3 that follows gives what it gives for the fp32 quotients.
+// The product with 1 / f is within 2.5 units in the last place of the quotient, and E4M3's rounding
+// borders (midpoints of its values, the subnormal ones too) have 19 zero bits at the end in fp32: a
+// product that is more than 3 units from such a number rounds alike.  A lane with another one, or
+// where 1 / f is not a normal number of usual size, divides.  (16 divisions for each K and V row took
+// 2.6 of 18.7 us for 4099 tokens of 32 + 2 x 4 heads.)
+__device__ __forceinline__ void divide(float (&a)[8], float (&b)[8], float f) {
+  const float inv = 1.f / f;
+  float qa[8], qb[8];
+  uint32_t least = 0xffffffffu;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    qa[e] = a[e] * inv, qb[e] = b[e] * inv;
+    least = min(least, min((__float_as_uint(qa[e]) + 3) & 0x7ffffu, (__float_as_uint(qb[e]) + 3) & 0x7ffffu));
+  }
+  const bool exact = (__float_as_uint(f) & 0x7fffffu) == 0;  // a power of two: so is the product
+  const bool usual = fabsf(f) > 1e-30f && fabsf(f) < 1e30f;
+  if (__builtin_expect(usual && (exact || least >= 7), 1)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = qa[e], b[e] = qb[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] /= f, b[e] /= f;
+  }
+}
+
 enum Mode { kTrain, kCacheBf16, kCacheE4m3 };
 
 // Forward.  A run of D/16 lanes per (token, run of heads_per_unit heads); heads count q's, then
@@ -319,11 +345,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const NormRop
       } else {
         // the value over its head's factor, rounded once to E4M3 (saturating)
         const float* ds = kind == 2 ? a.v_descale : a.k_descale;
-        if (ds) {
-          const float f = __ldg(ds + h);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ya[e] /= f, yb[e] /= f;
-        }
+        if (ds) divide(ya, yb, __ldg(ds + h));
         *reinterpret_cast<uint2*>(dst + 8 * t.ca) = pack8_e4m3(ya);
         *reinterpret_cast<uint2*>(dst + 8 * t.cb) = pack8_e4m3(yb);
       }
