@@ -349,8 +349,8 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
 /*
  * A paged key/value cache for serving (the pages have no counterpart): K and V live in two pools
  * of num_pages pages of page_size tokens, [num_pages, page_size, Hk, d] by common strides c_sp,
- * c_st, c_sh (elements) of page, token and head, d contiguous, every stride a multiple of 16
- * bytes.  cache_fp8 = 0: bf16; 1: E4M3 codes standing for code * descale[head] (k_descale,
+ * c_st, c_sh (elements, not negative) of page, token and head, d contiguous, every stride a
+ * multiple of 16 bytes.  cache_fp8 = 0: bf16; 1: E4M3 codes standing for code * descale[head] (k_descale,
  * v_descale: fp32 [Hk], or NULL for 1).  A request's tokens are at the pages that its row of the
  * block table names: token j in page table[j / page_size], at j % page_size; slot = page *
  * page_size + offset.  page_size and num_pages: any values >= 1 (page_size * num_pages < 2^62).

@@ -51,6 +51,7 @@ bool cache_ok(const void* k, const void* v, int num_pages, int page_size, int Hk
               long long c_sh, int size) {
   if (!rows_ok(k, true) || !rows_ok(v, true) || num_pages < 1 || page_size < 1) return false;
   const long long unit = 16 / size;
+  if (c_sp < 0 || c_st < 0 || c_sh < 0) return false;
   return stride_ok(c_sp, num_pages, unit) && stride_ok(c_st, page_size, unit) && stride_ok(c_sh, Hk, unit);
 }
 

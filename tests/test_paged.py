@@ -84,7 +84,7 @@ def _append(**kw):
 @pytest.mark.parametrize("kw,code", [
     *((dict([(n, 0)]), INVALID) for n in ("q", "k", "v", "rope", "pos", "slots", "qo", "kc", "vc", "rows", "pages", "ps")),
     (dict(kc=A16 + 8), INVALID), (dict(slots=A16 + 4), INVALID), (dict(fp8=2), INVALID), (dict(kd=A16), INVALID),
-    (dict(fp8=1, vd=A16 + 2), INVALID), (dict(fp8=1, cs=(2048, 128, 72)), INVALID), (dict(cs=(2044, 128, 64)), INVALID),
+    (dict(fp8=1, vd=A16 + 2), INVALID), (dict(fp8=1, cs=(2048, 128, 72)), INVALID), (dict(cs=(2044, 128, 64)), INVALID), (dict(cs=(-2048, 128, 64)), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(rot=24), UNSUPPORTED), (dict(rot=66), INVALID), (dict(T=-1), INVALID),
     (dict(qs=(255, 64)), INVALID), (dict(vs=(128, 4)), INVALID), (dict(eps=-1.0), INVALID), (dict(T=0), OK)])
 def test_append_refuses(kw, code):
@@ -107,7 +107,7 @@ def _dec(**kw):
     (dict(ws=A16 + 16), INVALID), (dict(wsb=1000), INVALID), (dict(Hq=3), INVALID), (dict(d=80), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(T=-1), INVALID),
     (dict(rows=7), INVALID), (dict(ts=7), INVALID), (dict(kd=A16), INVALID), (dict(fp8=3), INVALID),
-    (dict(cs=(2048, 100, 64)), INVALID), (dict(qs=(256, 63)), INVALID),
+    (dict(cs=(2048, 100, 64)), INVALID), (dict(cs=(2048, -128, 64)), INVALID), (dict(qs=(256, 63)), INVALID),
     (dict(cols=1 << 20, ts=1 << 20, ps=1 << 11), INVALID), (dict(T=0), OK), (dict(Hq=0), OK)])
 def test_decode_refuses(kw, code):
     assert _dec(**kw) == code
