@@ -495,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const Nor
 }
 
 // dw[i] = sum over the blocks of its kind of partial[block][i], 32 columns per block, in a fixed
-// order: blockIdx.x is the columns, blockIdx.y 0 for q, 1 for k.
+// order: blockIdx.x is the columns, blockIdx.y 0 for q, 1 for k.  A thread's share of 592 partials is
+// two batches of loads: latency is all there is to this kernel (2 us behind the first one's end).
+constexpr int kDwBatch = 10;
 __global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* partial, int blocks_q, int blocks, int d,
                                                                float* dwq, float* dwk) {
   __shared__ float red[32][33];
@@ -503,10 +505,15 @@ __global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* part
   float* const out = blockIdx.y == 0 ? dwq : dwk;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!out) return;
+  const int end = blockIdx.y == 0 ? blocks_q : blocks;
   float s = 0.f;
-#pragma unroll 8
-  for (int r = (blockIdx.y == 0 ? 0 : blocks_q) + y; r < (blockIdx.y == 0 ? blocks_q : blocks); r += 32)
-    s += partial[(size_t)r * d + col];
+  for (int r0 = (blockIdx.y == 0 ? 0 : blocks_q) + y; r0 < end; r0 += 32 * kDwBatch) {
+    float v[kDwBatch];
+#pragma unroll
+    for (int i = 0; i < kDwBatch; ++i) v[i] = partial[(size_t)min(r0 + 32 * i, end - 1) * d + col];
+#pragma unroll
+    for (int i = 0; i < kDwBatch; ++i) s += r0 + 32 * i < end ? v[i] : 0.f;
+  }
   red[y][c] = s;
   __syncthreads();
   float v = red[c][y];  // warp y now holds column y's 32 sums
