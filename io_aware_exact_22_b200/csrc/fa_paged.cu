@@ -395,6 +395,10 @@ __device__ __forceinline__ Part part_of(void* ws, int ctas) {
   return r;
 }
 
+__device__ __forceinline__ void write_lse(const DecodeArgs& a, long long t, int h, float m, float l, float bias) {
+  a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l) - bias) * 0.6931471805599453f;
+}
+
 // Finishes one output row's 4 elements: o = sum / l, and the row's LSE (once per row).
 template <int D>
 __device__ __forceinline__ void write_out(const DecodeArgs& a, long long t, int h, int c4, float4 x, float m, float l,
@@ -404,7 +408,7 @@ __device__ __forceinline__ void write_out(const DecodeArgs& a, long long t, int 
   u.x = pack_bf16(x.x * inv, x.y * inv);
   u.y = pack_bf16(x.z * inv, x.w * inv);
   *reinterpret_cast<uint2*>(a.o + (t * a.Hq + h) * D + c4 * 4) = u;
-  if (c4 == 0) a.lse[t * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l) - bias) * 0.6931471805599453f;
+  if (c4 == 0) write_lse(a, t, h, m, l, bias);
 }
 
 // The reference max of a query row moves only when a score exceeds it by more than 2^kSlack, so P
@@ -750,9 +754,6 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
           for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
           if (g8 == 0) s_m[warp][8 * n + 2 * i4 + e] = m[n][e], s_l[warp][8 * n + 2 * i4 + e] = l[n][e];
         }
-      // through the stage just read, which is filled again only after the last barrier here
-      float* join = reinterpret_cast<float*>(smem + stage * C::STAGE);
-      constexpr int RS = C::RS, WS = kStages * C::STAGE / 4;
       const bool whole = seg_end && seg_tile0 == 0;
       const int slot = 2 * cta + (seg_tile0 == 0 ? 1 : 0);
       if (tid == 0 && seg_tile0 == 0 && (by_group || left == 0)) {  // the group began here: is it divided?
@@ -762,47 +763,68 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
         part.head[by_group ? cur.t * groups + cur.hm : cta] =
             whole ? make_int4(-1, 0, 0, 0) : make_int4(cur.t, cur.hm, cta, (int)holder);
       }
-      __syncwarp();
+      __syncthreads();
+      // lane r of each warp: the max and sum of its head's query row r over the warps, and what its
+      // own warp's O is to be multiplied by, so that the warps' O only have to be added
+      float fac = 0.f;
+      if (lane < 8 * NQ) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if ((w & (a.hp - 1)) == hw) M = fmaxf(M, s_m[w][lane]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = s_m[w][lane], f = mw == -INFINITY ? (M == -INFINITY ? 1.f : 0.f) : ex2(mw - M);
+          if ((w & (a.hp - 1)) == hw) L = fmaf(f, s_l[w][lane], L);
+          if (w == warp) fac = f;
+        }
+        if (whole) fac *= L > 0.f || L != L ? (FP8 && a.vd ? __ldg(a.vd + hk) : 1.f) / L : 0.f;
+        if (kw == 0 && lane < rows) {
+          if (whole) write_lse(a, cur.t, hk * g + row0 + lane, M, L, FP8 ? kPBias : 0.f);
+          else part.ml[((size_t)slot * a.hp + hw) * kMaxRows + lane] = make_float2(M, L);
+        }
+      }
+      // through the stage just read, which is filled again only after the last barrier here
+      float* join = reinterpret_cast<float*>(smem + stage * C::STAGE);
+      constexpr int RS = C::RS, WS = kStages * C::STAGE / 4;
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const int nrows = min(8, rows - 8 * n);
         if (nrows <= 0) break;
         float* dst = join + warp * WS + 2 * i4 * RS;
 #pragma unroll
-        for (int c = 0; c < DC; ++c)
+        for (int e = 0; e < 2; ++e) {
+          const float f = __shfl_sync(0xffffffffu, fac, 8 * n + 2 * i4 + e);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int c = 0; c < DC; ++c) {
             if (FP8) {
-              *reinterpret_cast<float2*>(dst + e * RS + c * 16 + 2 * g8) = make_float2(acc[c][n][e], acc[c][n][e + 2]);
+              *reinterpret_cast<float2*>(dst + e * RS + c * 16 + 2 * g8) = make_float2(acc[c][n][e] * f, acc[c][n][e + 2] * f);
             } else {
-              dst[e * RS + c * 16 + g8] = acc[c][n][e];
-              dst[e * RS + c * 16 + g8 + 8] = acc[c][n][e + 2];
+              dst[e * RS + c * 16 + g8] = acc[c][n][e] * f;
+              dst[e * RS + c * 16 + g8 + 8] = acc[c][n][e + 2] * f;
             }
           }
-        __syncthreads();
-        for (int i = tid; i < a.hp * nrows * (D / 4); i += kWarps * 32) {
-          const int hr = i / (D / 4), c4 = i % (D / 4), h = hr / nrows, row = hr - h * nrows;
-          float M = -INFINITY;
-          for (int w = h; w < kWarps; w += a.hp) M = fmaxf(M, s_m[w][8 * n + row]);
-          float L = 0.f;
-          float4 o = make_float4(0, 0, 0, 0);
-          for (int w = h; w < kWarps; w += a.hp) {
-            const float mw = s_m[w][8 * n + row];
-            const float f = mw == -INFINITY ? (M == -INFINITY ? 1.f : 0.f) : ex2(mw - M);
-            const float4 v = *reinterpret_cast<const float4*>(join + w * WS + row * RS + c4 * 4);
-            L = fmaf(f, s_l[w][8 * n + row], L);
-            o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
-          }
-          if (whole) {
-            const int kvh = hg * a.hp + h;
-            const float vscale = FP8 && a.vd ? __ldg(a.vd + kvh) : 1.f;
-            write_out<D>(a, cur.t, kvh * g + row0 + 8 * n + row, c4, o, M, L, vscale, FP8 ? kPBias : 0.f);
-          } else {
-            const size_t pr = ((size_t)slot * a.hp + h) * kMaxRows + 8 * n + row;
-            *reinterpret_cast<float4*>(part.o + pr * D + c4 * 4) = o;
-            if (c4 == 0) part.ml[pr] = make_float2(M, L);
-          }
         }
+        __syncthreads();
+        const int c4 = tid % (D / 4);
+        for (int h = 0; h < a.hp; ++h)
+#pragma unroll 2
+          for (int row = tid / (D / 4); row < nrows; row += kWarps * 32 / (D / 4)) {
+            float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+              if ((w & (a.hp - 1)) == h) {
+                const float4 v = *reinterpret_cast<const float4*>(join + w * WS + row * RS + c4 * 4);
+                o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+              }
+            if (whole) {
+              const long long at = cur.t * (long long)a.Hq + (hg * a.hp + h) * g + row0 + 8 * n + row;
+              *reinterpret_cast<uint2*>(a.o + at * D + c4 * 4) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            } else {
+              const size_t pr = ((size_t)slot * a.hp + h) * kMaxRows + 8 * n + row;
+              *reinterpret_cast<float4*>(part.o + pr * D + c4 * 4) = o;
+            }
+          }
         __syncthreads();
       }
       fresh = true;
