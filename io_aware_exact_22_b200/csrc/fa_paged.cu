@@ -538,8 +538,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
           cp_async16(dst + KEYS * ROWB, src + vk, there ? 16 : 0);
         }
       }
-      --fetch_left;
-      cursor_next(a, ahead, groups, shift);
+      if (--fetch_left > 0) cursor_next(a, ahead, groups, shift);
     }
     cp_commit();
     lookup();
