@@ -374,7 +374,7 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  *   plan_status        : out, int32 [1]: 0, or the FA_PLAN_* reasons why the step cannot be
  *                        planned; then nothing changes (lens = cached, free_count_out =
  *                        free_count, cu_tokens 0, slots -1)
- * table_cols * page_size <= FA_PAGED_MAX_LEN, max_tokens <= FA_PAGED_MAX_LEN (it may be 0).  Pointers 4-byte aligned, slots 8.
+ * table_cols * page_size, pool_pages and max_tokens (it may be 0) are at most FA_PAGED_MAX_LEN.  Pointers 4-byte aligned, slots 8.
  *
  * fa_paged_append: the norm and rotation of fa_qk_norm_rope for T tokens, with the keys and the
  * values written to the cache.

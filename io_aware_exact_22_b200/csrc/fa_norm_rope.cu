@@ -557,7 +557,11 @@ BwdBlocks bwd_blocks(long long tokens, int Hq, int Hk, int d) {
   r.per = heads_per_unit(runs, Hq + Hk);
   constexpr int all = 148 * 4, W = kThreads / 32;
   auto need = [&](int H) { return (runs * ((H + r.per - 1) / r.per) + W - 1) / W; };
-  const int share = Hq + Hk > 0 ? (int)(((long long)all * Hq + (Hq + Hk) / 2) / (Hq + Hk)) : 0;
+  // a unit costs its heads and about kUnitStart more: positions and the table's row come first
+  constexpr int kUnitStart = 3;
+  auto cost = [&](int H) { return H == 0 ? 0LL : H + kUnitStart * (long long)((H + r.per - 1) / r.per); };
+  const long long cq = cost(Hq), both = cq + cost(Hk);
+  const int share = both > 0 ? (int)((all * cq + both / 2) / both) : 0;
   r.q = Hq == 0 ? 0 : (int)std::min<long long>(std::min(std::max(share, 1), Hk ? all - 1 : all), need(Hq));
   r.k = Hk == 0 ? 0 : (int)std::min<long long>(std::max(all - share, 1), need(Hk));
   return r;

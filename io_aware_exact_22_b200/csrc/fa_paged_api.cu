@@ -140,7 +140,8 @@ fa_status_t fa_paged_plan(const int* cached, const int* new_tokens, int* block_t
                           int* free_count_out, int* plan_status, void* stream) {
   if (R < 0 || max_tokens < 0 || table_cols < 0 || pool_pages < 0 || page_size < 1) return FA_ERR_INVALID_ARG;
   if (R > FA_PLAN_MAX_REQUESTS) return FA_ERR_UNSUPPORTED;
-  if ((long long)table_cols * page_size > FA_PAGED_MAX_LEN || max_tokens > FA_PAGED_MAX_LEN)
+  if ((long long)table_cols * page_size > FA_PAGED_MAX_LEN || max_tokens > FA_PAGED_MAX_LEN ||
+      pool_pages > FA_PAGED_MAX_LEN)
     return FA_ERR_INVALID_ARG;
   if (!free_count || !cu_tokens || !free_count_out || !plan_status) return FA_ERR_INVALID_ARG;
   if (R > 0 && (!cached || !new_tokens || !lens || (table_cols > 0 && !block_table))) return FA_ERR_INVALID_ARG;

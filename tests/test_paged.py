@@ -66,7 +66,7 @@ def _plan(**kw):
     (dict(cached=A16 + 2), INVALID), (dict(slots=A16 + 4), INVALID), (dict(ps=0), INVALID), (dict(R=-1), INVALID),
     (dict(most=-1), INVALID), (dict(cols=-1), INVALID), (dict(pool=-1), INVALID), (dict(ts=7), INVALID),
     (dict(R=fa.PLAN_MAX_REQUESTS + 1), UNSUPPORTED), (dict(cols=1 << 20, ts=1 << 20, ps=1 << 12), INVALID),
-    (dict(most=fa.PAGED_MAX_LEN + 1), INVALID), (dict(cols=1, ts=1, ps=fa.PAGED_MAX_LEN + 1), INVALID)])
+    (dict(most=fa.PAGED_MAX_LEN + 1), INVALID), (dict(pool=fa.PAGED_MAX_LEN + 1), INVALID), (dict(cols=1, ts=1, ps=fa.PAGED_MAX_LEN + 1), INVALID)])
 def test_plan_refuses(kw, code):
     assert _plan(**kw) == code
 
@@ -165,7 +165,7 @@ def _check_plan(cached, new, table, free, ps, most):
 @pytest.mark.parametrize("R,maxlen,chunk,gone,ps,extra", [
     (1, 0, 1, 0, 16, 0), (1, 40, 1, 0, 1, 3), (16, 300, 1, 0, 16, 0), (33, 90, 40, 5, 24, 7), (31, 500, 9, 2, 7, 1),
     (1023, 60, 3, 4, 16, 100), (1025, 60, 3, 4, 16, 100), (2500, 20, 2, 3, 4, 9), (70, 700, 700, 6, 64, 40),
-    (3, 0, 30000, 0, 16, 5), (5, 10, 1, 1, 8, 4), (fa.PLAN_MAX_REQUESTS, 3, 1, 3, 2, 0)])
+    (3, 0, 30000, 0, 16, 5), (5, 10, 1, 1, 8, 4), (50, 20000, 2, 2, 1, 3), (fa.PLAN_MAX_REQUESTS, 3, 1, 3, 2, 0)])
 def test_plan(cuda_ok, R, maxlen, chunk, gone, ps, extra):
     rng = np.random.default_rng(R + ps)
     cached = rng.integers(0, maxlen + 1, R).tolist()
