@@ -159,7 +159,7 @@ struct NormRopeBwdArgs {
   long long q_sb, q_sn, q_sh, k_sb, k_sn, k_sh, dq_sb, dq_sn, dq_sh, dk_sb, dk_sn, dk_sh, pos_sb;
   int B, N, Hq, Hk, rot, rope_rows;
   float eps;
-  int heads_per_unit, blocks_q;      // set by the launcher
+  int per_q, per_k, blocks_q;        // set by the launcher: heads per unit, blocks that take q
 };
 // mode: 0 training form, 1 bf16 cache, 2 E4M3 cache
 cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream);

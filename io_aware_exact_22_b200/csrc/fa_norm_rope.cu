@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const Nor
   const bool is_q = (int)blockIdx.x < a.blocks_q;
   const int block = is_q ? blockIdx.x : blockIdx.x - a.blocks_q;
   const int blocks = is_q ? a.blocks_q : gridDim.x - a.blocks_q;
-  const int H = is_q ? a.Hq : a.Hk, chunks = (H + a.heads_per_unit - 1) / a.heads_per_unit;
+  const int H = is_q ? a.Hq : a.Hk, per = is_q ? a.per_q : a.per_k, chunks = (H + per - 1) / per;
   const long long tokens = (long long)a.B * a.N, units = (tokens + G - 1) / G * chunks;
   const __nv_bfloat16* const xs = is_q ? a.q : a.k;
   const __nv_bfloat16* const gs = is_q ? a.gq : a.gk;
@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const Nor
   auto enter = [&](Place& p) {  // the first head of p.unit
     const long long run = quotient(p.unit, chunks);
     p.tok = run * G + lane / LPR;
-    p.h = (int)(p.unit - run * chunks) * a.heads_per_unit;
-    p.h1 = min(H, p.h + a.heads_per_unit);
+    p.h = (int)(p.unit - run * chunks) * per;
+    p.h1 = min(H, p.h + per);
     if (p.tok < tokens) {
       p.b = (int)quotient(p.tok, a.N), p.n = (int)(p.tok - (long long)p.b * a.N);
       p.x = xs + p.b * (is_q ? a.q_sb : a.k_sb) + p.n * (is_q ? a.q_sn : a.k_sn) + p.h * x_sh;
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_bwd_kernel(const Nor
   for (long long unit = (long long)block * W + warp; unit < units; unit += (long long)blocks * W) {
     const long long run = quotient(unit, chunks);
     const long long tok = run * G + lane / LPR;
-    const int h0 = (int)(unit - run * chunks) * a.heads_per_unit, h1 = min(H, h0 + a.heads_per_unit);
+    const int h0 = (int)(unit - run * chunks) * per, h1 = min(H, h0 + per);
     bool go = tok < tokens;
     const int b = go ? (int)quotient(tok, a.N) : 0, n = go ? (int)(tok - (long long)b * a.N) : 0;
     int pos = n;
@@ -528,18 +528,18 @@ __global__ void __launch_bounds__(1024) fa_norm_rope_dw_kernel(const float* part
 // 16 take 88 us, 32 take 94 and 8 take 97; at 4192 tokens of 40 heads, where 10 are 1.8 waves, 20
 // are one.
 constexpr int kMaxHeads = 16, kStart = 6, kWarpSlots = 148 * 16;
-int heads_per_unit(long long token_runs, int heads) {
-  const int most = std::min(heads, kMaxHeads);
-  const long long units = token_runs * ((heads + most - 1) / most);
-  if (units >= 4 * kWarpSlots) return most;
+int heads_per_unit(long long token_runs, int heads, int slots) {
+  const int least = (heads + kMaxHeads - 1) / kMaxHeads, most = (heads + least - 1) / least;  // runs of one length
+  const long long units = token_runs * least;
+  if (units >= 4LL * slots) return most;
   int best = most;
-  long long cost = (units + kWarpSlots - 1) / kWarpSlots * (most + kStart);
+  long long cost = (units + slots - 1) / slots * (most + kStart);
   for (int waves = 1; waves <= 4; ++waves) {
-    const long long chunks = std::min<long long>(heads, (long long)waves * kWarpSlots / token_runs);
+    const long long chunks = std::min<long long>(heads, (long long)waves * slots / token_runs);
     if (chunks < 1) continue;
     const int per = (int)((heads + chunks - 1) / chunks);
     const long long n = token_runs * ((heads + per - 1) / per);
-    const long long c = (n + kWarpSlots - 1) / kWarpSlots * (per + kStart);
+    const long long c = (n + slots - 1) / slots * (per + kStart);
     if (c < cost) cost = c, best = per;
   }
   return best;
@@ -547,23 +547,31 @@ int heads_per_unit(long long token_runs, int heads) {
 
 long long token_runs(long long tokens, int d) { return (tokens + 32 / (d / 16) - 1) / (32 / (d / 16)); }
 
-// Blocks of the backward kernel: four per SM, shared out by heads, and no more than there are units.
+// Blocks of the backward kernel: four per SM and no more than there are units.  Warps are shared out
+// between q and k by what their units cost (heads, and about kUnitStart more: positions and the
+// table's row come first), then k's are set to whole rounds over its units.  Measured against shares
+// by heads alone: B=4 N=6900, 16 + 1 heads, d=64: 53 -> 35 us.
 struct BwdBlocks {
-  int per, q, k;
+  int per_q, per_k, q, k;
 };
 BwdBlocks bwd_blocks(long long tokens, int Hq, int Hk, int d) {
-  BwdBlocks r;
+  constexpr int all = 148 * 4, W = kThreads / 32, kUnitStart = 3;
   const long long runs = token_runs(tokens, d);
-  r.per = heads_per_unit(runs, Hq + Hk);
-  constexpr int all = 148 * 4, W = kThreads / 32;
-  auto need = [&](int H) { return (runs * ((H + r.per - 1) / r.per) + W - 1) / W; };
-  // a unit costs its heads and about kUnitStart more: positions and the table's row come first
-  constexpr int kUnitStart = 3;
-  auto cost = [&](int H) { return H == 0 ? 0LL : H + kUnitStart * (long long)((H + r.per - 1) / r.per); };
-  const long long cq = cost(Hq), both = cq + cost(Hk);
-  const int share = both > 0 ? (int)((all * cq + both / 2) / both) : 0;
-  r.q = Hq == 0 ? 0 : (int)std::min<long long>(std::min(std::max(share, 1), Hk ? all - 1 : all), need(Hq));
-  r.k = Hk == 0 ? 0 : (int)std::min<long long>(std::max(all - share, 1), need(Hk));
+  auto per = [&](int H) {
+    return H == 0 ? 1 : heads_per_unit(runs, H, std::max<long long>(W, (long long)kWarpSlots * H / (Hq + Hk)));
+  };
+  BwdBlocks r = {per(Hq), per(Hk), 0, 0};
+  const long long uq = runs * ((Hq + r.per_q - 1) / r.per_q), uk = runs * ((Hk + r.per_k - 1) / r.per_k);
+  auto blocks = [&](long long warps) { return (int)std::min<long long>(all, (warps + W - 1) / W); };
+  const double cq = (double)runs * Hq + (double)kUnitStart * uq, ck = (double)runs * Hk + (double)kUnitStart * uk;
+  if (Hq == 0 || Hk == 0) {
+    r.q = blocks(uq), r.k = blocks(uk);
+    return r;
+  }
+  const double share = std::max(1.0, all * W * ck / (cq + ck));  // k's warps
+  const long long rounds = std::max(1LL, (long long)(uk / share + 0.5));
+  r.k = std::min(blocks((uk + rounds - 1) / rounds), all - 1);
+  r.q = std::min(blocks(uq), all - r.k);
   return r;
 }
 
@@ -577,7 +585,7 @@ int norm_rope_bwd_blocks(long long tokens, int Hq, int Hk, int d) {
 cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream) {
   const int heads = a.Hq + a.Hk * (mode == kTrain ? 1 : 2);
   const long long runs = token_runs((long long)a.B * a.N, d);
-  a.heads_per_unit = heads_per_unit(runs, heads);
+  a.heads_per_unit = heads_per_unit(runs, heads, kWarpSlots);
   a.chunks = (heads + a.heads_per_unit - 1) / a.heads_per_unit;
   const long long blocks = (runs * a.chunks + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
@@ -603,7 +611,7 @@ cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, 
 cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, float* dwq, float* dwk,
                                  cudaStream_t stream) {
   const BwdBlocks r = bwd_blocks((long long)a.B * a.N, a.Hq, a.Hk, d);
-  a.heads_per_unit = r.per, a.blocks_q = r.q;
+  a.per_q = r.per_q, a.per_k = r.per_k, a.blocks_q = r.q;
   const int blocks = r.q + r.k;
 #define FA_NRB(DD, II) fa_norm_rope_bwd_kernel<DD, II><<<blocks, kThreads, 0, stream>>>(a)
   if (d == 64) {
