@@ -7,7 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -78,9 +78,14 @@ void* vec_or_null(PyObject* o, const char* name, at::ScalarType type, int index,
   return o == Py_None ? nullptr : vec(o, name, type, index, numel);
 }
 
+// A new contiguous tensor, without a detour through the dispatcher.
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
+  return Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt));
+}
+
 // An output: the caller's contiguous tensor, checked, or a new one.
 Tensor output(PyObject* o, const char* name, at::ScalarType type, int index, at::IntArrayRef shape) {
-  if (o == Py_None) return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, index));
+  if (o == Py_None) return fresh(shape, type, index);
   const Tensor& t = tensor(o, name);
   TORCH_CHECK_VALUE(t.scalar_type() == type && on(t, index) && t.sizes() == shape && t.is_contiguous(), name,
                     " must be a contiguous ", type, " tensor ", shape, " on CUDA device ", index);
@@ -277,15 +282,14 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float eps = number(a[8]);
   const int inter = truth(a[9]);
   auto gradient = [&](PyObject* o, const char* name, const Tensor& like) {
-    if (o == Py_None) return at::empty(like.sizes(), at::TensorOptions().dtype(at::kBFloat16).device(at::kCUDA, x.index));
+    if (o == Py_None) return fresh(like.sizes(), at::kBFloat16, x.index);
     const Tensor& t = rows(o, name, 4, x.index);
     TORCH_CHECK_VALUE(t.sizes() == like.sizes(), name, " must have the shape ", like.sizes());
     distinct(t, name);
     return t;
   };
   const Tensor dq = gradient(a[10], "dq", x.q), dk = gradient(a[11], "dk", x.k);
-  const auto f32 = at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, x.index);
-  const Tensor dwq = at::empty({x.d}, f32), dwk = at::empty({x.d}, f32);
+  const Tensor dwq = fresh({x.d}, at::kFloat, x.index), dwk = fresh({x.d}, at::kFloat, x.index);
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
   const Workspace ws(a[12], c_norm_rope_bwd_bytes(x.B, x.N, x.Hq, x.Hk, x.d), x.index);
   const fa_status_t st = launch(x.index, [&](void* stream) {
