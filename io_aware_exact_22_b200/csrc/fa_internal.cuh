@@ -163,10 +163,14 @@ struct NormRopeBwdArgs {
 };
 // mode: 0 training form, 1 bf16 cache, 2 E4M3 cache
 cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream);
-// Blocks of the backward kernel, i.e. rows of its partial weight gradients.
-int norm_rope_bwd_blocks(long long tokens, int Hq, int Hk, int d);
-cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, float* dwq, float* dwk,
-                                 cudaStream_t stream);
+// How the backward kernel goes over a problem: heads per unit, and blocks that take q and k, i.e. rows
+// of the partial weight gradients.
+struct NormRopeBwdPlan {
+  int per_q, per_k, q, k;
+};
+NormRopeBwdPlan norm_rope_bwd_plan(long long tokens, int Hq, int Hk, int d);
+cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, const NormRopeBwdPlan& plan, float* dwq,
+                                 float* dwk, cudaStream_t stream);
 
 // ------------------------------------------------------------------ paged cache (fa_paged.cu)
 struct PlanArgs {

@@ -547,20 +547,19 @@ int heads_per_unit(long long token_runs, int heads, int slots) {
 
 long long token_runs(long long tokens, int d) { return (tokens + 32 / (d / 16) - 1) / (32 / (d / 16)); }
 
+}  // namespace
+
 // Blocks of the backward kernel: four per SM and no more than there are units.  Warps are shared out
 // between q and k by what their units cost (heads, and about kUnitStart more: positions and the
 // table's row come first), then k's are set to whole rounds over its units.  Measured against shares
 // by heads alone: B=4 N=6900, 16 + 1 heads, d=64: 53 -> 35 us.
-struct BwdBlocks {
-  int per_q, per_k, q, k;
-};
-BwdBlocks bwd_blocks(long long tokens, int Hq, int Hk, int d) {
+NormRopeBwdPlan norm_rope_bwd_plan(long long tokens, int Hq, int Hk, int d) {
   constexpr int all = 148 * 4, W = kThreads / 32, kUnitStart = 3;
   const long long runs = token_runs(tokens, d);
   auto per = [&](int H) {
     return H == 0 ? 1 : heads_per_unit(runs, H, std::max<long long>(W, (long long)kWarpSlots * H / (Hq + Hk)));
   };
-  BwdBlocks r = {per(Hq), per(Hk), 0, 0};
+  NormRopeBwdPlan r = {per(Hq), per(Hk), 0, 0};
   const long long uq = runs * ((Hq + r.per_q - 1) / r.per_q), uk = runs * ((Hk + r.per_k - 1) / r.per_k);
   auto blocks = [&](long long warps) { return (int)std::min<long long>(all, (warps + W - 1) / W); };
   const double cq = (double)runs * Hq + (double)kUnitStart * uq, ck = (double)runs * Hk + (double)kUnitStart * uk;
@@ -573,13 +572,6 @@ BwdBlocks bwd_blocks(long long tokens, int Hq, int Hk, int d) {
   r.k = std::min(blocks((uk + rounds - 1) / rounds), all - 1);
   r.q = std::min(blocks(uq), all - r.k);
   return r;
-}
-
-}  // namespace
-
-int norm_rope_bwd_blocks(long long tokens, int Hq, int Hk, int d) {
-  const BwdBlocks r = bwd_blocks(tokens, Hq, Hk, d);
-  return r.q + r.k;
 }
 
 cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream) {
@@ -608,9 +600,8 @@ cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, float* dwq, float* dwk,
-                                 cudaStream_t stream) {
-  const BwdBlocks r = bwd_blocks((long long)a.B * a.N, a.Hq, a.Hk, d);
+cudaError_t launch_norm_rope_bwd(int d, bool interleaved, NormRopeBwdArgs a, const NormRopeBwdPlan& r, float* dwq,
+                                 float* dwk, cudaStream_t stream) {
   a.per_q = r.per_q, a.per_k = r.per_k, a.blocks_q = r.q;
   const int blocks = r.q + r.k;
 #define FA_NRB(DD, II) fa_norm_rope_bwd_kernel<DD, II><<<blocks, kThreads, 0, stream>>>(a)
