@@ -21,8 +21,8 @@
 //
 // Bound by HBM.  On a B200, replayed from a graph: B=1 N=16384, 64 heads, d=128 takes 87 us (6.2 TB/s,
 // 0.95 of a copy; rows loaded to registers, two to four ahead, took 115 to 148), its gradient at B=2
-// N=4096, 32 heads 38.5 us (5.3 TB/s, of which 2 us add up the weights' gradients), the cache form
-// with 4099 tokens of 40 heads to E4M3 16 us (5.1 TB/s, from L2 in part: one wave of warps, whose slots,
+// N=4096, 32 heads 37.3 us (5.5 TB/s, of which 2 us add up the weights' gradients), the cache form
+// with 4099 tokens of 40 heads to E4M3 15.2 us (5.4 TB/s, from L2 in part: one wave of warps, whose slots,
 // positions and table rows come one after the other), 8 tokens 3.0 us.
 #include "fa_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -552,7 +552,8 @@ long long token_runs(long long tokens, int d) { return (tokens + 32 / (d / 16) -
 // Blocks of the backward kernel: four per SM and no more than there are units.  Warps are shared out
 // between q and k by what their units cost (heads, and about kUnitStart more: positions and the
 // table's row come first), then k's are set to whole rounds over its units.  Measured against shares
-// by heads alone: B=4 N=6900, 16 + 1 heads, d=64: 53 -> 35 us.
+// by heads alone: B=4 N=6900, 16 + 1 heads, d=64: 53 -> 38 us; one number of heads per unit for both,
+// the larger share's: B=4 N=1017, 32 + 8 heads: 31 -> 25 us.
 NormRopeBwdPlan norm_rope_bwd_plan(long long tokens, int Hq, int Hk, int d) {
   constexpr int all = 148 * 4, W = kThreads / 32, kUnitStart = 3;
   const long long runs = token_runs(tokens, d);

@@ -17,7 +17,7 @@ using namespace ptx;
 // Requests hold cached[b] tokens in ceil(cached[b] / page_size) pages; the step adds
 // new_tokens[b] tokens, or releases the request (-1).  Released pages go on top of the free stack
 // in the order (request, page), wanted pages come off its top in the same order, so the result
-// depends on the inputs alone.  Bound by latency: 3.2 us for 16 decoding requests, 9.8 us for 1000
+// depends on the inputs alone.  Bound by latency: 3.4 us for 16 decoding requests, 9.9 us for 1000
 // mixed ones with 50 k tokens.  Everything is one kernel: every block of one cluster scans the
 // requests for itself (a few bytes each, from L2), the cluster's barrier separates reading the
 // inputs from writing, which is what lets the outputs alias them, and then the tokens are spread
