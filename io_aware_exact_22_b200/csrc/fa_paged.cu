@@ -259,9 +259,10 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
 // up to 8 heads cost no empty rows, K and V (and their conversion from E4M3) are read from shared
 // memory once for 16 heads, and O takes D / 4 registers for 8 heads.  K and V come once from memory
 // and feed 4 g flops per element, an order of magnitude below what the tensor pipe needs to be the
-// bound at the copy bandwidth.  P is kept to 16 bits: in bf16 as the sum of two bf16 terms (a high
-// and a low part, so the product's rounding stays below the output's), with an E4M3 cache, whose
-// values are exact in fp16, as one fp16 term.
+// bound at the copy bandwidth.  P is the sum of two terms, a high and a low part, each with a product
+// of its own: bf16 terms (16 bits, so the product's rounding stays below the output's), with an E4M3
+// cache, whose values are exact in fp16, fp16 terms (22 bits; one term of 11 bits changed the rounded
+// outputs by 9e-4 in relative norm and took the same time: 105 us for the E4M3 case below).
 //
 // Bound by HBM once contexts are long; about 8 us go to the launches, to the chain of lengths, pages
 // and keys, and to the join.  On a B200, replayed from a graph: 2 x 131071 keys, 32 query and 4 kv heads,
@@ -350,6 +351,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ float2 unpack_f16(uint32_t u) {
+  float2 f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(u));
+  return f;
+}
 
 // Number of keys of query row t; 0 writes an empty row's result, -1 leaves the row as it was.
 // `r` is its row of the block table.
@@ -431,8 +439,8 @@ __device__ __forceinline__ void write_out(const DecodeArgs& a, long long t, int 
 
 // The reference max of a query row moves only when a score exceeds it by more than 2^kSlack, so P
 // stays below 2^kSlack, and most tiles need no reduction over lanes and no rescaling of O.  P of
-// the E4M3 form carries the power of two kPBias: at most 2^15 in fp16, and held to full precision
-// down to 2^-21 of the row's largest.
+// the E4M3 form carries the power of two kPBias: at most 2^15 in fp16, and its low term held to 11 bits
+// down to 2^-10 of the row's largest, below that to 2^-32 of it.
 constexpr float kSlack = 8.f;
 constexpr float kPBias = 7.f;
 
@@ -718,7 +726,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (FP8) {
-              hi[n][h] = transpose8(pack_f16(p[2 * h], p[2 * h + 1]));
+              const uint32_t u = pack_f16(p[2 * h], p[2 * h + 1]);
+              const float2 f = unpack_f16(u);
+              hi[n][h] = transpose8(u);
+              lo[n][h] = transpose8(pack_f16(p[2 * h] - f.x, p[2 * h + 1] - f.y));
             } else {
               const uint32_t u = pack_bf16(p[2 * h], p[2 * h + 1]);
               hi[n][h] = transpose8(u);
@@ -752,7 +763,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
               const uint32_t u0 = __byte_perm(r[2 * e], 0, 0x3120), u1 = __byte_perm(r[2 * e + 1], 0, 0x3120);
               const uint32_t a0 = e4m3_lo(u0), a1 = e4m3_hi(u0), a2 = e4m3_lo(u1), a3 = e4m3_hi(u1);
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) mma16816<true>(acc[c + e][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+              for (int n = 0; n < NQ; ++n) {
+                mma16816<true>(acc[c + e][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+                mma16816<true>(acc[c + e][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+              }
             }
           }
         }

@@ -1,0 +1,106 @@
+"""Precision of the paged decode, on problems whose terms cancel: the values of a row's keys are chosen so
+that sum_j p_j V_j nearly vanishes, so that the rounding of O does not hide what becomes of P.
+
+Tolerance of `cancelling`.  Scores are one product each, exact in fp32, of base-2 size below 0.12, and 5
+keys at most fall into one step of the matrix unit.  Relative error of p_j: the scale and its product,
+2 u 0.12; the difference to the reference, u 0.12 (E4M3: it carries the power 2^7, u 8 in the reference
+and as much in the difference, u = 2^-24); the exponential 2^-22; the terms that P is split into, 2^-24
+(three of bf16) or 2^-22 (two of fp16): together below 2^-21 (bf16) and 2^-20 (E4M3).  The matrix unit
+may cut each of 5 products and the sum to 24 bits of the largest, which is at most half of
+mag = sum p_j |V_j|: 6 2^-23 / 2 mag, below 2^-21.4.  The factors to 1 / l and the store are relative
+to O, which is near zero: 2^-8 of it and 2^-20 more.  So |error| <= 2^-20 mag (bf16), 2^-19 mag (E4M3), and
+2^-8 |O|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from io_aware_exact_22_b200 import fa
+from oracle import paged_ref as ref
+from tests._helpers import f64
+
+OK = 0
+SCALE = 2.0 ** -6
+
+
+def _round_bf16(x):
+    return float(torch.tensor(x, dtype=torch.float64).bfloat16())
+
+
+E4M3_VALUES = np.unique([oracle.e4m3_decode(np.array([c], dtype=np.uint8))[0] for c in range(256) if c & 0x7f != 0x7f])
+
+
+def _round_e4m3(x):
+    return float(E4M3_VALUES[np.abs(E4M3_VALUES - x).argmin()])
+
+
+def cancelling(T, g, d, fp8, seed):
+    """q [T, g, d] bf16, k, v [T, n, d] fp64 of one kv head, values of the cache's type: the column c of V
+    makes sum_j p_j V_jc nearly zero for the query head c % g."""
+    rng = np.random.default_rng(seed)
+    n = 5 if fp8 else 3
+    q = np.zeros((T, g, d))
+    k, v = np.zeros((2, T, n, d))
+    q[:, :, 0] = rng.integers(128, 256, (T, g)) / 128 * rng.choice([-1, 1], (T, g))  # bf16 values in [1, 2)
+    k[:, :, 0] = rng.integers(8, 16, (T, n)) / 8 * rng.choice([-1, 1], (T, n))       # E4M3 values in [1, 2)
+    to = _round_e4m3 if fp8 else _round_bf16
+    for t in range(T):
+        p = np.exp(SCALE * np.outer(q[t, :, 0], k[t, :, 0]))  # [g, n]
+        for c in range(d):
+            w, total = p[c % g], 0.0
+            v[t, 0, c] = to(rng.uniform(200, 256) if fp8 else rng.uniform(1, 2))
+            for j in range(1, n):
+                total += w[j - 1] * v[t, j - 1, c]
+                v[t, j, c] = to(-total / w[j])
+    return q, k, v
+
+
+def test_the_problem_shows_the_split_of_p():
+    # with exact arithmetic but for P's terms: three bf16 terms and two fp16 terms pass, one fewer do not
+    def cut(p, kind, terms):
+        kept = np.zeros_like(p)
+        for _ in range(terms):
+            kept += torch.from_numpy(p - kept).to(kind).double().numpy()
+        return kept
+
+    for fp8, kind, terms, tol in ((False, torch.bfloat16, 3, 2.0 ** -20), (True, torch.float16, 2, 2.0 ** -19)):
+        q, k, v = cancelling(16, 4, 64, fp8, 3)
+        worst = []
+        for m in (terms, terms - 1):
+            over = 0.0
+            for t in range(16):
+                p = np.exp(SCALE * q[t, :, 0:1] * k[t, :, 0])
+                mag, want = p @ np.abs(v[t]), p @ v[t]
+                assert (np.abs(want) <= 2.0 ** -11 * mag)[np.arange(64) % 4, np.arange(64)].all()
+                over = max(over, ((np.abs(cut(p, kind, m) @ v[t] - want) - 2.0 ** -8 * np.abs(want)) / mag).max())
+            worst.append(over)
+        assert worst[0] < tol / 8 and worst[1] > 2 * tol, worst
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g", [(64, 4), (64, 12), (128, 4), (128, 16)])
+@pytest.mark.parametrize("fp8", [True])
+def test_probabilities_keep_fp32_precision(cuda_ok, fp8, d, g):
+    T, ps = 24, 16
+    q, k, v = cancelling(T, g, d, fp8, d + g)
+    n = k.shape[1]
+    kind = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    kc, vc = torch.zeros(2, T, ps, 1, d, dtype=torch.float32)
+    kc[:, :n, 0], vc[:, :n, 0] = torch.from_numpy(k).float(), torch.from_numpy(v).float()
+    kc, vc = kc.to(kind).cuda(), vc.to(kind).cuda()
+    assert np.array_equal(vc.float().double().cpu().numpy()[:, :n, 0], v)  # nothing was rounded
+    table = torch.arange(T, dtype=torch.int32, device="cuda")[:, None]
+    lens = torch.full((T,), n, dtype=torch.int32, device="cuda")
+    o, lse = fa.paged_decode(torch.from_numpy(q).bfloat16().cuda(), kc, vc, table, lens, scale=SCALE)
+    assert fa.fa_get_device_status() == OK
+    o, lse = f64(o), f64(lse)
+    tol = 2.0 ** -19 if fp8 else 2.0 ** -20
+    for t in range(T):
+        for h in range(g):
+            want, wl = ref.decode_row(q[t, h], k[t], v[t], SCALE)
+            mag = np.exp(SCALE * (k[t] @ q[t, h]) - wl) @ np.abs(v[t])
+            assert (np.abs(o[t, h] - want) <= 2.0 ** -8 * np.abs(want) + tol * mag).all(), (t, h)
+            assert abs(lse[t, h] - wl) <= 2.0 ** -19, (t, h)
