@@ -402,8 +402,8 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  *   workspace : fa_paged_decode_workspace_bytes(T, Hq, Hk, d) bytes (on the current device),
  *               256-byte aligned; contents on entry do not matter.  Concurrent calls (two
  *               captured graphs that may run at once, too) need distinct workspaces.
- * Hq a multiple of Hk; table_cols * page_size <= FA_PAGED_MAX_LEN.  P is a sum of two 16-bit terms (bf16 cache: bf16,
- * 16 bits in all; E4M3 cache: fp16, 22 bits); scores, maxima, sums and O are fp32.  A request row outside the table, a length
+ * Hq a multiple of Hk; table_cols * page_size <= FA_PAGED_MAX_LEN.  P is a sum of 16-bit terms (bf16 cache: three of
+ * bf16, 24 bits in all; E4M3 cache: two of fp16, 22 bits); scores, maxima, sums and O are fp32.  A request row outside the table, a length
  * outside [0, table_cols * page_size] or a page outside the pool sets the device status word; that
  * row's result is then not specified, the others' are not touched by it.  A NaN reaches its own
  * row's results; an infinite value makes its column infinite or NaN.  Equal calls give equal bits.

@@ -259,10 +259,10 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
 // up to 8 heads cost no empty rows, K and V (and their conversion from E4M3) are read from shared
 // memory once for 16 heads, and O takes D / 4 registers for 8 heads.  K and V come once from memory
 // and feed 4 g flops per element, an order of magnitude below what the tensor pipe needs to be the
-// bound at the copy bandwidth.  P is the sum of two terms, a high and a low part, each with a product
-// of its own: bf16 terms (16 bits, so the product's rounding stays below the output's), with an E4M3
-// cache, whose values are exact in fp16, fp16 terms (22 bits; one term of 11 bits changed the rounded
-// outputs by 9e-4 in relative norm and took the same time: 105 us for the E4M3 case below).
+// bound at the copy bandwidth.  P goes in as the sum of 16-bit terms, each with a
+// product of its own: three bf16 terms (24 bits), or, with an E4M3 cache, whose values are exact in fp16,
+// two fp16 terms (22 bits).  One term fewer changed the rounded outputs by 1e-4 and 9e-4 in relative norm
+// against 2e-5, for less than 1 % of the long cases' times below and 8 % with 16 heads per kv head.
 //
 // Bound by HBM once contexts are long; about 8 us go to the launches, to the chain of lengths, pages
 // and keys, and to the join.  On a B200, replayed from a graph: 2 x 131071 keys, 32 query and 4 kv heads,
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
       // O^T += V^T P^T, 16 keys at a time
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        uint32_t hi[NQ][2], lo[NQ][2];
+        uint32_t hi[NQ][2], lo[NQ][2], last[NQ][2];  // last: bf16 alone
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
           float p[4];
@@ -732,9 +732,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
               lo[n][h] = transpose8(pack_f16(p[2 * h] - f.x, p[2 * h + 1] - f.y));
             } else {
               const uint32_t u = pack_bf16(p[2 * h], p[2 * h + 1]);
+              const float r0 = p[2 * h] - __uint_as_float(u << 16), r1 = p[2 * h + 1] - __uint_as_float(u & 0xffff0000u);
+              const uint32_t v = pack_bf16(r0, r1);
               hi[n][h] = transpose8(u);
-              lo[n][h] = transpose8(pack_bf16(p[2 * h] - __uint_as_float(u << 16),
-                                              p[2 * h + 1] - __uint_as_float(u & 0xffff0000u)));
+              lo[n][h] = transpose8(v);
+              last[n][h] = transpose8(pack_bf16(r0 - __uint_as_float(v << 16), r1 - __uint_as_float(v & 0xffff0000u)));
             }
           }
         }
@@ -748,6 +750,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
             for (int n = 0; n < NQ; ++n) {
               mma16816<false>(acc[c][n], r[0], r[1], r[2], r[3], hi[n][0], hi[n][1]);
               mma16816<false>(acc[c][n], r[0], r[1], r[2], r[3], lo[n][0], lo[n][1]);
+              mma16816<false>(acc[c][n], r[0], r[1], r[2], r[3], last[n][0], last[n][1]);
             }
           }
         } else {

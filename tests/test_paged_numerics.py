@@ -82,7 +82,7 @@ def test_the_problem_shows_the_split_of_p():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("d,g", [(64, 4), (64, 12), (128, 4), (128, 16)])
-@pytest.mark.parametrize("fp8", [True])
+@pytest.mark.parametrize("fp8", [False, True])
 def test_probabilities_keep_fp32_precision(cuda_ok, fp8, d, g):
     T, ps = 24, 16
     q, k, v = cancelling(T, g, d, fp8, d + g)
