@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
 // memory once for 16 heads, and O takes D / 4 registers for 8 heads.  K and V come once from memory
 // and feed 4 g flops per element, an order of magnitude below what the tensor pipe needs to be the
 // bound at the copy bandwidth.  P goes in as the sum of 16-bit terms, each with a
-// product of its own: three bf16 terms (24 bits), or, with an E4M3 cache, whose values are exact in fp16,
+// product of its own: three bf16 terms (to 2^-23), or, with an E4M3 cache, whose values are exact in fp16,
 // two fp16 terms (22 bits).  One term fewer changed the rounded outputs by 1e-4 and 9e-4 in relative norm
 // against 2e-5, for less than 1 % of the long cases' times below and 8 % with 16 heads per kv head.
 //
@@ -357,6 +357,16 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t u) {
       : "=f"(f.x), "=f"(f.y)
       : "r"(u));
   return f;
+}
+// The largest value of 8 bits below x > 0 (0 for 0).  A split of P by it leaves no term zero or
+// negative, so that an infinite V stays infinite through all their products.
+__device__ __forceinline__ float below(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return __uint_as_float((u - min(u, 1u)) & 0xffff0000u);
+}
+// Two values of 8 bits as bf16.
+__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
 // Number of keys of query row t; 0 writes an empty row's result, -1 leaves the row as it was.
@@ -731,12 +741,11 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
               hi[n][h] = transpose8(u);
               lo[n][h] = transpose8(pack_f16(p[2 * h] - f.x, p[2 * h + 1] - f.y));
             } else {
-              const uint32_t u = pack_bf16(p[2 * h], p[2 * h + 1]);
-              const float r0 = p[2 * h] - __uint_as_float(u << 16), r1 = p[2 * h + 1] - __uint_as_float(u & 0xffff0000u);
-              const uint32_t v = pack_bf16(r0, r1);
-              hi[n][h] = transpose8(u);
-              lo[n][h] = transpose8(v);
-              last[n][h] = transpose8(pack_bf16(r0 - __uint_as_float(v << 16), r1 - __uint_as_float(v & 0xffff0000u)));
+              const float p0 = p[2 * h], p1 = p[2 * h + 1], a0 = below(p0), a1 = below(p1);
+              const float r0 = p0 - a0, r1 = p1 - a1, b0 = below(r0), b1 = below(r1);
+              hi[n][h] = transpose8(high_halves(a0, a1));
+              lo[n][h] = transpose8(high_halves(b0, b1));
+              last[n][h] = transpose8(pack_bf16(r0 - b0, r1 - b1));
             }
           }
         }

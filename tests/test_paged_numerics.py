@@ -4,7 +4,7 @@ that sum_j p_j V_j nearly vanishes, so that the rounding of O does not hide what
 Tolerance of `cancelling`.  Scores are one product each, exact in fp32, of base-2 size below 0.12, and 5
 keys at most fall into one step of the matrix unit.  Relative error of p_j: the scale and its product,
 2 u 0.12; the difference to the reference, u 0.12 (E4M3: it carries the power 2^7, u 8 in the reference
-and as much in the difference, u = 2^-24); the exponential 2^-22; the terms that P is split into, 2^-24
+and as much in the difference, u = 2^-24); the exponential 2^-22; the terms that P is split into, 2^-23
 (three of bf16) or 2^-22 (two of fp16): together below 2^-21 (bf16) and 2^-20 (E4M3).  The matrix unit
 may cut each of 5 products and the sum to 24 bits of the largest, which is at most half of
 mag = sum p_j |V_j|: 6 2^-23 / 2 mag, below 2^-21.4.  The factors to 1 / l and the store are relative
@@ -104,3 +104,44 @@ def test_probabilities_keep_fp32_precision(cuda_ok, fp8, d, g):
             mag = np.exp(SCALE * (k[t] @ q[t, h]) - wl) @ np.abs(v[t])
             assert (np.abs(o[t, h] - want) <= 2.0 ** -8 * np.abs(want) + tol * mag).all(), (t, h)
             assert abs(lse[t, h] - wl) <= 2.0 ** -19, (t, h)
+
+def _cache(lens, ps, d, seed):
+    """Block table and bf16 caches of one kv head, pages in random order, what no key uses NaN."""
+    rng, g = np.random.default_rng(seed), torch.Generator().manual_seed(seed)
+    need = [-(-n // ps) for n in lens]
+    pages = rng.permutation(sum(need)).tolist()
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    kc, vc = (torch.randn(sum(need), ps, 1, d, generator=g).bfloat16() for _ in range(2))
+    for t, n in enumerate(lens):
+        mine = [pages.pop() for _ in range(need[t])]
+        table[t, :need[t]] = torch.tensor(mine, dtype=torch.int32)
+        if n % ps:
+            kc[mine[-1], n % ps:] = vc[mine[-1], n % ps:] = math.nan
+    return table.cuda(), kc.cuda(), vc.cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("equal", [True, False])
+@pytest.mark.parametrize("d,g,lens", [(64, 2, [1, 5, 200]), (128, 12, [3, 90, 17]), (128, 4, [20000, 2, 700])])
+def test_infinite_values_are_as_the_formula_has_them(cuda_ok, d, g, lens, equal):
+    # every key has a positive probability (equal scores: a power of two), so a column with +inf is +inf, with
+    # -inf -inf, with both NaN; the others are as without them
+    T, ps = len(lens), 16
+    table, kc, vc = _cache(lens, ps, d, 7)
+    q = torch.randn(T, g, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda() * (0 if equal else 1)
+    args = (table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    clean, lse = fa.paged_decode(q, kc, vc, *args)
+    for t, n in enumerate(lens):
+        first, last = table[t, 0].item(), table[t, (n - 1) // ps].item()
+        vc[first, 0, 0, 3] = math.inf
+        vc[last, (n - 1) % ps, 0, 8] = -math.inf
+        vc[last, (n - 1) % ps, 0, d - 1] = math.inf
+        if n > 1:
+            vc[first, 0, 0, d - 1] = -math.inf
+    got, l2 = fa.paged_decode(q, kc, vc, *args)
+    assert fa.fa_get_device_status() == OK and torch.equal(lse, l2)
+    keep = [c for c in range(d) if c not in (3, 8, d - 1)]
+    assert torch.equal(got[:, :, keep], clean[:, :, keep])
+    assert (got[:, :, 3] == math.inf).all() and (got[:, :, 8] == -math.inf).all()
+    for t, n in enumerate(lens):
+        assert torch.isnan(got[t, :, d - 1]).all() if n > 1 else (got[t, :, d - 1] == math.inf).all()
