@@ -403,7 +403,8 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  *               256-byte aligned; contents on entry do not matter.  Concurrent calls (two
  *               captured graphs that may run at once, too) need distinct workspaces.
  * Hq a multiple of Hk; table_cols * page_size <= FA_PAGED_MAX_LEN.  P is a sum of 16-bit terms (bf16 cache: three of
- * bf16, to 2^-23; E4M3 cache: two of fp16, 22 bits); scores, maxima, sums and O are fp32.  A request row outside the table, a length
+ * bf16, to 2^-23; E4M3 cache: two of fp16, 22 bits); with an E4M3 cache q
+ * is exact down to 2^-32 of its row's largest element, and to 2^-40 of it below; scores, maxima, sums and O are fp32.  A request row outside the table, a length
  * outside [0, table_cols * page_size] or a page outside the pool sets the device status word; that
  * row's result is then not specified, the others' are not touched by it.  A NaN reaches its own
  * row's results; an infinite value makes its column infinite, or NaN where one of the other sign meets it

@@ -632,8 +632,9 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
         if (!FP8) {
           sc[n][0] = sc[n][1] = a.scale_log2;
         } else {
-          // q to fp16 exactly but for elements 2^-24 below the row's largest: the row is scaled
-          // by a power of two that brings that one into [1, 2)
+          // q to fp16: the row is scaled by a power of two that brings its largest element into
+          // [2^15, 2^16), where bf16's 8 bits still end at fp16's largest value.  Elements are then exact
+          // down to 2^-32 of that one, and to 2^-40 of it below (fp16's smallest step is 2^-24).
           float big = 0.f;
 #pragma unroll
           for (int s = 0; s < DC; ++s)
@@ -642,8 +643,8 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
               big = fmaxf(big, fmaxf(fabsf(__uint_as_float(qb[s][n][e] << 16)), fabsf(__uint_as_float(qb[s][n][e] & 0xffff0000u))));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          const int e = min(max((int)(__float_as_uint(big) >> 23), 2), 252);  // biased exponent
-          const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = __uint_as_float((uint32_t)e << 23);
+          const int e = min(max((int)(__float_as_uint(big) >> 23), 16), 254);  // biased exponent
+          const float down = __uint_as_float((uint32_t)(269 - e) << 23), up = __uint_as_float((uint32_t)(e - 15) << 23);
 #pragma unroll
           for (int s = 0; s < DC; ++s)
 #pragma unroll

@@ -145,3 +145,32 @@ def test_infinite_values_are_as_the_formula_has_them(cuda_ok, d, g, lens, equal)
     assert (got[:, :, 3] == math.inf).all() and (got[:, :, 8] == -math.inf).all()
     for t, n in enumerate(lens):
         assert torch.isnan(got[t, :, d - 1]).all() if n > 1 else (got[t, :, d - 1] == math.inf).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,g", [(64, 2), (128, 12)])
+@pytest.mark.parametrize("small", [2.0 ** -12, 2.0 ** -20])
+def test_a_large_channel_of_q_leaves_the_small_ones_exact(cuda_ok, d, g, small):
+    # E4M3 cache, one channel of q 2^22 or 2^30 times the others, which meets keys that are 0 there.  Tolerance
+    # as in test_paged.py, E = 4 d u A + 4 n u with 2^-20 for the exponential and P; q's elements
+    # lie above 2^-32 of the largest and are exact
+    n, ps, T = 40, 16, 3
+    rng = torch.Generator().manual_seed(d)
+    table, kc, vc = _cache([n] * T, ps, d, 4)
+    kc, vc = ((64 * c.float()).clamp(-448, 448).nan_to_num(0.0).to(torch.float8_e4m3fn) for c in (kc, vc))
+    kc.view(torch.uint8)[..., 5] = 0
+    q = ((1 + torch.rand(T, g, d, generator=rng)) * small).bfloat16()
+    q[..., 5] = 1024.0
+    scale = 2.0 ** -8 / small
+    o, lse = fa.paged_decode(q.cuda(), kc, vc, table, torch.full((T,), n, dtype=torch.int32, device="cuda"), scale=scale)
+    assert fa.fa_get_device_status() == OK
+    k, v = (c.float().double().cpu().numpy() for c in (kc, vc))
+    q64, o, lse, tab = f64(q), f64(o), f64(lse), table.cpu().numpy()
+    for t in range(T):
+        kk, vv = (ref.gather(c, tab[t], n, 0, ps) for c in (k, v))
+        for h in range(g):
+            want, wl = ref.decode_row(q64[t, h], kk, vv, scale)
+            E = 4 * d * 2.0 ** -24 * scale * (np.abs(kk) @ np.abs(q64[t, h])).max() + 2.0 ** -20 + 4 * n * 2.0 ** -24
+            mag = np.exp(scale * (kk @ q64[t, h]) - wl) @ np.abs(vv)
+            assert (np.abs(o[t, h] - want) <= 2.0 ** -8 * np.abs(want) + E * mag).all(), (t, h)
+            assert abs(lse[t, h] - wl) <= E + 2.0 ** -22 * abs(wl), (t, h)
