@@ -328,8 +328,8 @@ fa_status_t fa_bwd_dq_post(const void* workspace, size_t workspace_bytes, void* 
  * q_out, k_out).  dq, dk: bf16 [B, N, H, d] by their own strides; dwq, dwk: fp32 [d], summed over
  * all rows in a fixed order (equal calls give equal bits), or NULL.  All are overwritten; dwq and
  * dwk are zeroed for an empty problem.  A token whose position is outside the table adds nothing.
- *   workspace : fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d) bytes, 256-byte aligned;
- *               contents on entry do not matter.  Concurrent calls need distinct workspaces.
+ *   workspace : fa_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hk, d) bytes (the same for every
+ *               problem of one d that is not empty), 256-byte aligned; contents on entry do not matter.  Concurrent calls need distinct workspaces.
  */
 fa_status_t fa_qk_norm_rope(const void* q, const void* k, const void* wq, const void* wk, const float* rope,
                             int rope_rows, int rot, int interleaved, const int* positions, long long pos_sb,

@@ -164,7 +164,8 @@ struct NormRopeBwdArgs {
 // mode: 0 training form, 1 bf16 cache, 2 E4M3 cache
 cudaError_t launch_norm_rope(int d, bool interleaved, int mode, NormRopeArgs a, cudaStream_t stream);
 // How the backward kernel goes over a problem: heads per unit, and blocks that take q and k, i.e. rows
-// of the partial weight gradients.
+// of the partial weight gradients (kNormRopeBwdBlocks at most).
+constexpr int kNormRopeBwdBlocks = 148 * 4;
 struct NormRopeBwdPlan {
   int per_q, per_k, q, k;
 };

@@ -555,7 +555,7 @@ long long token_runs(long long tokens, int d) { return (tokens + 32 / (d / 16) -
 // by heads alone: B=4 N=6900, 16 + 1 heads, d=64: 53 -> 38 us; one number of heads per unit for both,
 // the larger share's: B=4 N=1017, 32 + 8 heads: 31 -> 25 us.
 NormRopeBwdPlan norm_rope_bwd_plan(long long tokens, int Hq, int Hk, int d) {
-  constexpr int all = 148 * 4, W = kThreads / 32, kUnitStart = 3;
+  constexpr int all = kNormRopeBwdBlocks, W = kThreads / 32, kUnitStart = 3;
   const long long runs = token_runs(tokens, d);
   auto per = [&](int H) {
     return H == 0 ? 1 : heads_per_unit(runs, H, std::max<long long>(W, (long long)kWarpSlots * H / (Hq + Hk)));

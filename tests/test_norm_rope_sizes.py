@@ -177,3 +177,24 @@ def test_append(cuda_ok, T, Hq, Hk, d, rot, inter, fp8, heads_outer):
     rest = rest.nonzero()[:, 0]
     for c in (kc, vc):  # other slots are as they were
         assert (as_bits(c)[rest // ps, rest % ps] == fill).all()
+
+
+def test_workspace_size_does_not_shrink_as_the_problem_grows():
+    n = fa.fa_qk_norm_rope_bwd_workspace_bytes
+    for d in (64, 128):
+        for Hq, Hk in ((1, 0), (16, 16), (32, 8), (35, 5)):
+            sizes = [n(1, N, Hq, Hk, d) for N in (1, 5, 100, 1000, 2368, 2372, 4096, 4100, 16384, 100000)]
+            assert sizes == sorted(sizes) and sizes[0] > 0
+    assert n(1, 2368, 16, 16, 128) <= n(2, 4096, 16, 16, 128) and n(1, 100, 8, 2, 64) <= n(1, 100, 32, 8, 64)
+
+
+@pytest.mark.gpu
+def test_one_workspace_serves_shorter_sequences(cuda_ok):
+    # sized for the longest of them, handed to all
+    H, d = 16, 128
+    ws = torch.full((fa.fa_qk_norm_rope_bwd_workspace_bytes(1, 2372, H, H, d),), 0xff, dtype=torch.uint8, device="cuda")
+    for N in (2372, 2368, 700, 1):
+        q, k, gq, gk = (torch.randn(*s, d, device="cuda").bfloat16() for s in ((1, N, H), (1, N, H), (1, H, N), (1, H, N)))
+        want = fa.qk_norm_rope_backward(gq, gk, q, k, None, None, None)
+        got = fa.qk_norm_rope_backward(gq, gk, q, k, None, None, None, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
