@@ -5,7 +5,8 @@ visit counters, see include/fa.h).
     python -m io_aware_exact_22_b200.build [--force] [--verbose] [--debug | --all]
 
 libfa.so comes with _fa_torch.so, the extension of the binding (csrc/fa_torch.cpp, host code only,
-compiled against the torch that runs the build).
+compiled against the torch that runs the build; without torch the build says so and makes the library
+alone).
 
 Each .cu file under csrc/ is compiled to an object in _build/ (skipped when the object is
 newer than every source and header), then linked into one shared library against the static
@@ -64,8 +65,12 @@ def _stale(target: str, deps) -> bool:
 def _build_ext(force: bool, verbose: bool) -> None:
     import sysconfig
 
-    import torch
-
+    try:
+        import torch
+    except ImportError as e:
+        print(f"{os.path.basename(EXT)} (the binding's norm + rotation and paged calls) is not built: no torch here ({e})",
+              file=sys.stderr)
+        return
     base = os.path.dirname(torch.__file__)
     if not force and not _stale(EXT, [EXT_SRC, os.path.join(INCLUDE, "fa.h"), torch.__file__]):
         return
