@@ -189,7 +189,8 @@ struct Cache {
                           (type == at::kBFloat16 || type == at::kFloat8_e4m3fn || type == at::kByte) && k.stride(3) == 1,
                       "k_cache, v_cache must be bf16 or E4M3 tensors [pages, page_size, Hk, d] of one shape, the last "
                       "dimension contiguous, on CUDA device ", index);
-    TORCH_CHECK_VALUE(v.strides() == k.strides(), "k_cache and v_cache must have the same strides");
+    for (int64_t i = 0; i < 4; ++i)  // (of one element, the stride is not looked at)
+      TORCH_CHECK_VALUE(k.size(i) <= 1 || v.stride(i) == k.stride(i), "k_cache and v_cache must have the same strides");
     fp8 = type != at::kBFloat16;
     pages = i32(k.size(0), "pages"), page_size = i32(k.size(1), "page_size"), Hk = i32(k.size(2), "heads");
     d = i32(k.size(3), "d");
