@@ -7,7 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -78,9 +78,9 @@ void* vec_or_null(PyObject* o, const char* name, at::ScalarType type, int index,
   return o == Py_None ? nullptr : vec(o, name, type, index, numel);
 }
 
-// A new contiguous tensor, without a detour through the dispatcher.
+// A new contiguous tensor, by torch's dispatcher: its modes (a fill of uninitialised memory, say) see it.
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int index) {
-  return Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt));
+  return at::empty(shape, at::device(at::Device(at::kCUDA, static_cast<at::DeviceIndex>(index))).dtype(type));
 }
 
 // An output: the caller's contiguous tensor, checked, or a new one.

@@ -40,3 +40,29 @@ def test_different_strides_are_refused(cuda_ok):
     with pytest.raises(ValueError):
         fa.paged_decode(torch.zeros(1, 2, 64, device="cuda", dtype=torch.bfloat16), kc, vc,
                         torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.gpu
+def test_new_outputs_take_torchs_fill_of_uninitialised_memory(cuda_ok):
+    # as forward's do: with torch's deterministic fill, rows that a call leaves as they were are NaN
+    d = 64
+    kc, vc = torch.randn(2, 4, 16, 2, d, device="cuda").bfloat16()
+    q, x = torch.randn(40, 4, d, device="cuda").bfloat16(), torch.randn(1, 40, 6, d, device="cuda").bfloat16()
+    table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    ints = lambda v: torch.full((40,), v, dtype=torch.int32, device="cuda")  # noqa: E731
+    for shape in ((40, 4, d), (1, 4, 40, d), (1, 2, 40, d), (1, 40, 4, d), (1, 40, 2, d)):  # blocks that are handed out again
+        torch.full(shape, 5.0, device="cuda", dtype=torch.bfloat16)
+    before = torch.are_deterministic_algorithms_enabled()
+    torch.use_deterministic_algorithms(True)
+    try:
+        assert torch.utils.deterministic.fill_uninitialized_memory
+        o, lse = fa.paged_decode(q, kc, vc, table, ints(3), req=ints(-1))
+        qo = fa.paged_append(q, x[0, :, :2], x[0, :, :2], None, None, None, None, ints(-1).long(), kc, vc)
+        rope = fa.rope_table(8, d)
+        a, b = fa.qk_norm_rope(x[:, :, :4], x[:, :, 4:], None, None, rope, ints(9))  # no position is in the table
+        dq, dk, _, _ = fa.qk_norm_rope_backward(a, b, x[:, :, :4], x[:, :, 4:], None, None, rope, ints(9))
+    finally:
+        torch.use_deterministic_algorithms(before)
+    assert fa.fa_get_device_status() == 5  # the positions
+    for t in (o, lse, qo, a, b, dq, dk):
+        assert torch.isnan(t).all()
