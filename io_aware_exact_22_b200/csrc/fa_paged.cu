@@ -329,6 +329,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with sums that begin at zero.
+template <bool F16>
+__device__ __forceinline__ void mma16816_new(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // Two E4M3 codes (the low or the high 16 bits) to two fp16 values, exactly.
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
   uint32_t r;
@@ -721,10 +734,10 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
             for (int c = 0; c < DC; ++c) acc[c][n][e] *= al, acc[c][n][e + 2] *= al;
           }
       }
-      // O^T += V^T P^T, 16 keys at a time
+      // P: its terms for every 16 keys, transposed
+      uint32_t hi[MT][NQ][2], lo[MT][NQ][2], last[MT][NQ][2];  // last: bf16 alone
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        uint32_t hi[NQ][2], lo[NQ][2], last[NQ][2];  // last: bf16 alone
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
           float p[4];
@@ -739,34 +752,50 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
             if (FP8) {
               const uint32_t u = pack_f16(p[2 * h], p[2 * h + 1]);
               const float2 f = unpack_f16(u);
-              hi[n][h] = transpose8(u);
-              lo[n][h] = transpose8(pack_f16(p[2 * h] - f.x, p[2 * h + 1] - f.y));
+              hi[t][n][h] = transpose8(u);
+              lo[t][n][h] = transpose8(pack_f16(p[2 * h] - f.x, p[2 * h + 1] - f.y));
             } else {
               const float p0 = p[2 * h], p1 = p[2 * h + 1], a0 = below(p0), a1 = below(p1);
               const float r0 = p0 - a0, r1 = p1 - a1, b0 = below(r0), b1 = below(r1);
-              hi[n][h] = transpose8(high_halves(a0, a1));
-              lo[n][h] = transpose8(high_halves(b0, b1));
-              last[n][h] = transpose8(pack_bf16(r0 - b0, r1 - b1));
+              hi[t][n][h] = transpose8(high_halves(a0, a1));
+              lo[t][n][h] = transpose8(high_halves(b0, b1));
+              last[t][n][h] = transpose8(pack_bf16(r0 - b0, r1 - b1));
             }
           }
         }
-        if (!FP8) {
-          const int row = t * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+      // O^T += V^T P^T.  The matrix unit cuts its sums instead of rounding them, and what it cuts off a long
+      // sum adds up (3e-5 of it over 128 tiles), so a tile's products are summed apart, the smallest
+      // terms first, and added to O with rounding; 1 % of the long cases' times.
+      if (!FP8) {
+        const int half = (lane >> 3) & 1;
 #pragma unroll
-          for (int c = 0; c < DC; ++c) {
+        for (int c = 0; c < DC; ++c) {
+          float x[NQ][4];
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const int row = t * 16 + (lane & 7) + ((lane >> 4) << 3);
             uint32_t r[4];
             ldsm4t(r, vb + row * ROWB + (((2 * c + half) ^ swz<CH>(row)) * 16));
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-              mma16816<false>(acc[c][n], r[0], r[1], r[2], r[3], hi[n][0], hi[n][1]);
-              mma16816<false>(acc[c][n], r[0], r[1], r[2], r[3], lo[n][0], lo[n][1]);
-              mma16816<false>(acc[c][n], r[0], r[1], r[2], r[3], last[n][0], last[n][1]);
+              if (t == 0) mma16816_new<false>(x[n], r[0], r[1], r[2], r[3], last[t][n][0], last[t][n][1]);
+              else mma16816<false>(x[n], r[0], r[1], r[2], r[3], last[t][n][0], last[t][n][1]);
+              mma16816<false>(x[n], r[0], r[1], r[2], r[3], lo[t][n][0], lo[t][n][1]);
+              mma16816<false>(x[n], r[0], r[1], r[2], r[3], hi[t][n][0], hi[t][n][1]);
             }
           }
-        } else {
-          const int row = t * 16 + (lane & 15);
 #pragma unroll
-          for (int c = 0; c < CH; c += 2) {
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[c][n][e] += x[n][e];
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < CH; c += 2) {
+          float x[2][NQ][4];
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const int row = t * 16 + (lane & 15);
             uint32_t r[4];
             ldsm4t(r, vb + row * ROWB + (((c + (lane >> 4)) ^ swz<CH>(row)) * 16));
 #pragma unroll
@@ -777,11 +806,18 @@ __global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_de
               const uint32_t a0 = e4m3_lo(u0), a1 = e4m3_hi(u0), a2 = e4m3_lo(u1), a3 = e4m3_hi(u1);
 #pragma unroll
               for (int n = 0; n < NQ; ++n) {
-                mma16816<true>(acc[c + e][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
-                mma16816<true>(acc[c + e][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+                if (t == 0) mma16816_new<true>(x[e][n], a0, a1, a2, a3, lo[t][n][0], lo[t][n][1]);
+                else mma16816<true>(x[e][n], a0, a1, a2, a3, lo[t][n][0], lo[t][n][1]);
+                mma16816<true>(x[e][n], a0, a1, a2, a3, hi[t][n][0], hi[t][n][1]);
               }
             }
           }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[c + e][n][k] += x[e][n][k];
         }
       }
     }

@@ -174,3 +174,35 @@ def test_a_large_channel_of_q_leaves_the_small_ones_exact(cuda_ok, d, g, small):
             mag = np.exp(scale * (kk @ q64[t, h]) - wl) @ np.abs(vv)
             assert (np.abs(o[t, h] - want) <= 2.0 ** -8 * np.abs(want) + E * mag).all(), (t, h)
             assert abs(lse[t, h] - wl) <= E + 2.0 ** -22 * abs(wl), (t, h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_sums_are_not_cut(cuda_ok, fp8):
+    # The scores of 16 keys, 1025 times over: with values of v, and -1024 v the last time.  O is 0 then, every
+    # p is off by the same wherever its score comes, and what the kernel gives is the error of its sums alone.
+    # In units of |v| sum p / l = |v|: 888 rows, two for each of 444 CTAs, so that a warp adds up a quarter of
+    # a row in 128 tiles of 32 keys.  Added with rounding, a tile costs u = 2^-24 of the warp's sum so far, half
+    # of a quarter on average: 64 u for the four warps.  Within a tile, 4 (E4M3) or 6 (bf16) steps of the matrix
+    # unit may each cut 2 u off the tile's own sum: 12 u over all tiles, and as much for the large last one.
+    # Below 128 u = 2^-17.  (Where each step is cut against the long sum, 512 or 768 steps lose about u
+    # of it each: 256 to 384 u.)
+    T, g, d, ps, n = 888, 4, 64, 16, 16 * 1025
+    rng = np.random.default_rng(6)
+    k0 = rng.integers(8, 16, ps) / 8 * rng.choice([-1, 1], ps)
+    v0 = rng.choice([-0.25, 0.25], d)
+    kind = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    kc, vc = torch.zeros(2, n // ps, ps, 1, d)
+    kc[..., 0] = torch.from_numpy(k0).float()[:, None]
+    vc[:] = torch.from_numpy(v0).float()
+    vc[-1] *= -1024
+    q = torch.zeros(T, g, d)
+    q[..., 0] = torch.from_numpy(rng.integers(128, 256, (T, g)) / 128)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    o, lse = fa.paged_decode(q.bfloat16().cuda(), kc.to(kind).cuda(), vc.to(kind).cuda(), ints([list(range(n // ps))]),
+                             ints([n] * T), req=ints([0] * T), scale=SCALE)
+    assert fa.fa_get_device_status() == OK
+    assert o.double().abs().max().item() <= 2.0 ** -17 * 0.25
+    want = np.log(1025 * np.exp(SCALE * f64(q[..., 0])[..., None] * k0).sum(-1))
+    # l: a lane adds up 512 terms (u of its sum each, half of it on average: 256 u = 2^-16), then 7 sums
+    assert np.abs(f64(lse) - want).max() <= 2.0 ** -15
