@@ -273,18 +273,21 @@ constexpr int kWarps = 4;
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxRows = 16;
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NQ>
 struct DecCfg {
   static constexpr int ROWB = D * (FP8 ? 1 : 2);          // bytes of a key's row
   static constexpr int CH = ROWB / 16;                    // 16-byte chunks of a row
   static constexpr int KEYS = ROWB == 256 ? 16 : 32;      // keys per warp and tile
   static constexpr int STAGE = 2 * KEYS * ROWB;           // K then V
   static constexpr int RPI = 32 / CH;                     // rows that one copy instruction covers
-  // More warps for bf16, more registers and bytes in flight per warp for E4M3, whose conversions are
-  // the longer chain: 3 CTAs of 2 stages against 2 of 3 take 51.7 and 53.5 us for 32 rows of 0-4096
-  // keys in bf16, 116.5 and 111.5 us for 64 rows of 1024-8192 keys in E4M3.
-  static constexpr int STAGES = FP8 ? 3 : 2;
-  static constexpr int CTAS = FP8 && D == 128 ? 2 : kMaxCtasPerSm;
+  // 2 CTAs of 3 stages per SM where a warp's registers want them (d = 128 with E4M3, whose conversions are the
+  // longer chain, or with 16 query heads, which spill at 3 CTAs), else 3, of 2 stages for bf16.  2 of 3
+  // against 3 of 2: bf16, d = 128, 16 heads per kv head, 32 x 4096 keys 41.8 and 45 us, 4 x 32768 36.7 and
+  // 39.3; up to 8 heads, 128 x 1024 keys 98.0 and 95.7, 32 x 0-4096 52.7 and 52.1 (but 2 x 131071 92.2
+  // and 94.5); E4M3, 64 x 1024-8192 keys 107.3 and 108.3, 16 heads 28 and 35.
+  static constexpr bool WIDE = D == 128 && (FP8 || NQ == 2);
+  static constexpr int STAGES = FP8 || WIDE ? 3 : 2;
+  static constexpr int CTAS = WIDE ? 2 : kMaxCtasPerSm;
   static constexpr int RS = D + 4;                        // floats of a row of O at the join: off one bank
   static constexpr int SMEM = kWarps * STAGES * STAGE;
   static_assert(8 * RS * 4 <= STAGE, "a stage holds 8 rows of a warp's O at the join");
@@ -468,8 +471,8 @@ constexpr float kSlack = 8.f;
 constexpr float kPBias = 7.f;
 
 template <int D, bool FP8, int NQ>
-__global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8>::CTAS) fa_paged_decode_kernel(const DecodeArgs a) {
-  using C = DecCfg<D, FP8>;
+__global__ void __launch_bounds__(kWarps * 32, DecCfg<D, FP8, NQ>::CTAS) fa_paged_decode_kernel(const DecodeArgs a) {
+  using C = DecCfg<D, FP8, NQ>;
   constexpr int KEYS = C::KEYS, MT = KEYS / 16, CH = C::CH, ROWB = C::ROWB;
   constexpr int kStages = C::STAGES;
   constexpr int DC = D / 16;  // 16-wide steps of the score product, and 16-row tiles of O^T
@@ -1019,7 +1022,7 @@ int decode_ctas(int per_sm) { return per_sm * sm_count(); }
 
 template <int D, bool FP8, int NQ>
 cudaError_t launch_decode_t(const DecodeArgs& a, cudaStream_t stream) {
-  using C = DecCfg<D, FP8>;
+  using C = DecCfg<D, FP8, NQ>;
   static_assert(C::CTAS * (C::SMEM + 2048) <= 228 * 1024, "CTAS CTAs fit an SM");
   static bool attr_set[64];
   int dev = 0;
