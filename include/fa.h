@@ -318,7 +318,8 @@ fa_status_t fa_bwd_dq_post(const void* workspace, size_t workspace_bytes, void* 
  *   rot         : 0 or a multiple of 16 up to d
  *   positions   : in,  int32 [B, N] with batch stride pos_sb (0: one row for every batch), or
  *                 NULL for position n at token n (then rope_rows >= N)
- *   q_out, k_out: out, bf16 [B, Hq, N, d] and [B, Hk, N, d], contiguous: what fa_fwd reads
+ *   q_out, k_out: out, bf16 [B, Hq, N, d] and [B, Hk, N, d], contiguous: what fa_fwd reads where Hk = Hq
+ *                 (it takes one number of heads: with fewer key heads, k_out and v are repeated for it)
  * Hq or Hk may be 0 (its pointers are then not looked at).  A position outside [0, rope_rows) sets
  * the device status word (FA_ERR_DEVICE_CHECK) and leaves the token's rows as they were.  Outputs
  * must not overlap inputs.  d in {64, 128}; pointers 16-byte aligned (positions 4); eps finite,
@@ -350,8 +351,8 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  * A paged key/value cache for serving (the pages have no counterpart): K and V live in two pools
  * of num_pages pages of page_size tokens, [num_pages, page_size, Hk, d] by common strides c_sp,
  * c_st, c_sh (elements, not negative) of page, token and head, d contiguous, every stride a
- * multiple of 16 bytes.  cache_fp8 = 0: bf16; 1: E4M3 codes standing for code * descale[head] (k_descale,
- * v_descale: fp32 [Hk], or NULL for 1).  A request's tokens are at the pages that its row of the
+ * multiple of 16 bytes.  cache_fp8 = 0: bf16; 1: E4M3 codes standing for code * descale[head]
+ * (k_descale, v_descale: fp32 [Hk], or NULL for 1).  A request's tokens are at the pages that its row of the
  * block table names: token j in page table[j / page_size], at j % page_size; slot = page *
  * page_size + offset.  page_size and num_pages: any values >= 1 (page_size * num_pages < 2^62).
  *
@@ -374,7 +375,8 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  *   plan_status        : out, int32 [1]: 0, or the FA_PLAN_* reasons why the step cannot be
  *                        planned; then nothing changes (lens = cached, free_count_out =
  *                        free_count, cu_tokens 0, slots -1)
- * table_cols * page_size, pool_pages and max_tokens (it may be 0) are at most FA_PAGED_MAX_LEN.  Pointers 4-byte aligned, slots 8.
+ * table_cols * page_size, pool_pages and max_tokens (it may be 0) are at most FA_PAGED_MAX_LEN.
+ * Pointers 4-byte aligned, slots 8.
  *
  * fa_paged_append: the norm and rotation of fa_qk_norm_rope for T tokens, with the keys and the
  * values written to the cache.
@@ -382,7 +384,7 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  *   wq, wk, rope, rot, interleaved, eps : as fa_qk_norm_rope (positions: int32 [T], required
  *               when rot > 0)
  *   slots     : in,  int64 [T]; a negative slot skips the token (its row of q_out stays as it
- *               was).  Two tokens with one slot: which is kept is not specified.
+ *               was).  Two tokens with one slot: for no element of it is specified whose is kept.
  *   q_out     : out, bf16 [T, Hq, d]
  *   k_cache, v_cache : in/out.  E4M3: value / descale rounded to nearest even, saturating.
  * A slot past the pool or a position outside the table sets the device status word and skips the
@@ -390,7 +392,9 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  *
  * fa_paged_decode: attention of one query token per row over the cache, split over the cache's
  * length so that every SM has equal work whatever the lengths are, and joined with the merge of
- * "Flash Attention" (special-jiahao.github.io, section 增量求解 softmax).
+ * "Flash Attention" (special-jiahao.github.io, section 增量求解 softmax).  Rows are independent: the tokens
+ * of a prompt's chunk, as rows of one request, each read its keys and values from the cache again, and
+ * so does every run of 16 of a kv head's query heads.
  *   q         : in,  bf16 [T, Hq, d] by strides q_st, q_sh; head h reads kv head h / (Hq / Hk)
  *   block_table: in, int32 [table_rows, table_cols], row stride table_stride; entries past a
  *               row's pages are not read
@@ -402,13 +406,14 @@ fa_status_t fa_qk_norm_rope_bwd(const void* gq, const void* gk, const void* q, c
  *   workspace : fa_paged_decode_workspace_bytes(T, Hq, Hk, d) bytes (on the current device),
  *               256-byte aligned; contents on entry do not matter.  Concurrent calls (two
  *               captured graphs that may run at once, too) need distinct workspaces.
- * Hq a multiple of Hk; table_cols * page_size <= FA_PAGED_MAX_LEN.  P is a sum of 16-bit terms (bf16 cache: three of
- * bf16, to 2^-23; E4M3 cache: two of fp16, 22 bits); with an E4M3 cache q
- * is exact down to 2^-32 of its row's largest element, and to 2^-40 of it below; scores, maxima, sums and O are fp32.  A request row outside the table, a length
- * outside [0, table_cols * page_size] or a page outside the pool sets the device status word; that
- * row's result is then not specified, the others' are not touched by it.  A NaN reaches its own
- * row's results; an infinite value makes its column infinite, or NaN where one of the other sign meets it
- * or its weight is below 2^-100 of the row's largest.  Equal calls give equal bits.
+ * Hq a multiple of Hk; table_cols * page_size <= FA_PAGED_MAX_LEN.  Scores, maxima, sums and O are
+ * fp32.  P is a sum of 16-bit terms (bf16 cache: three of bf16, to 2^-23; E4M3 cache: two of fp16, 22
+ * bits); with an E4M3 cache q is exact down to 2^-32 of its row's largest element, and to 2^-40 of it
+ * below.  A request row outside the table, a length outside [0, table_cols * page_size] or a page
+ * outside the pool sets the device status word; that row's result is then not specified, the others'
+ * are not touched by it.  A NaN reaches its own row's results; an infinite value makes its column
+ * infinite, or NaN where one of the other sign meets it or its weight is below 2^-100 of the row's
+ * largest.  Equal calls give equal bits.
  * Empty problems (T or R 0 with nothing to write, Hq + Hk 0) return FA_OK; errors as elsewhere.
  */
 #define FA_PLAN_MAX_REQUESTS 12288

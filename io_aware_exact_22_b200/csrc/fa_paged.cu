@@ -17,20 +17,20 @@ using namespace ptx;
 // Requests hold cached[b] tokens in ceil(cached[b] / page_size) pages; the step adds
 // new_tokens[b] tokens, or releases the request (-1).  Released pages go on top of the free stack
 // in the order (request, page), wanted pages come off its top in the same order, so the result
-// depends on the inputs alone.  Bound by latency: 3.4 us for 16 decoding requests, 9.9 us for 1000
+// depends on the inputs alone.  Bound by latency: 3.4 us for 16 decoding requests, 10.0 us for 1000
 // mixed ones with 50 k tokens.  Everything is one kernel: every block of one cluster scans the
 // requests for itself (a few bytes each, from L2), the cluster's barrier separates reading the
 // inputs from writing, which is what lets the outputs alias them, and then the tokens are spread
 // over all threads.  Nothing is written but `plan_status`, the unchanged lengths and the -1
 // padding when the step cannot be planned.
 constexpr int kPlanThreads = 1024;
-// Blocks of the cluster: 16 where the device can place such a cluster (beyond the portable 8): 1000
-// requests with 50 k tokens take 9.3 us, with 8 12.0.
+// Blocks of the cluster: 16 where the device can place such a cluster (beyond the portable 8), which
+// took a quarter off the mixed step's time (measured on an earlier form).
 constexpr int kPlanMaxCtas = 16;
 constexpr int kPlanRequests = 256;  // at most, per block: with released pages 1000 requests take 8.3 us on 4, 10.3 on 1
-// Neighbouring tokens (or pages) per thread: one search, one store per output.  1000 requests with
-// 50 k tokens take 12.0 us with 2, 14.2 with 1, 12.4 with 4 and 16.9 with 8 (the longer chain of
-// each thread shows); 100 requests of one token 3.3, 3.0, 3.8 and 5.0.
+// Neighbouring tokens (or pages) per thread: one search, one store per output.  Chosen on clusters of 8
+// blocks: 1000 requests with 50 k tokens took 12.0 us with 2, 14.2 with 1, 12.4 with 4 and 16.9 with 8
+// (the longer chain of each thread shows); 100 requests of one token 3.3, 3.0, 3.8 and 5.0.
 constexpr int kPlanPer = 2;
 constexpr int kPlanEach = 8;       // released pages per lane and turn, when there are many
 constexpr int kPlanPages = 16384;  // pages that may be released, per block
@@ -259,16 +259,21 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const PlanA
 // up to 8 heads cost no empty rows, K and V (and their conversion from E4M3) are read from shared
 // memory once for 16 heads, and O takes D / 4 registers for 8 heads.  K and V come once from memory
 // and feed 4 g flops per element, an order of magnitude below what the tensor pipe needs to be the
-// bound at the copy bandwidth.  P goes in as the sum of 16-bit terms, each with a
-// product of its own: three bf16 terms (to 2^-23), or, with an E4M3 cache, whose values are exact in fp16,
-// two fp16 terms (22 bits).  One term fewer changed the rounded outputs by 1e-4 and 9e-4 in relative norm
-// against 2e-5, for less than 1 % of the long cases' times below and 8 % with 16 heads per kv head.
+// bound at the copy bandwidth.  P goes in as the sum of 16-bit terms, each with a product of its own: three
+// bf16 terms (to 2^-23), or, with an E4M3 cache, whose values are exact in fp16, two fp16 terms (22 bits).
+// With one term fewer, and O as the matrix unit's own long sum (see there), the rounded outputs
+// differed from fp32 arithmetic's by 1e-4 (bf16) and 9e-4 (E4M3) in relative norm; they now differ by less
+// than 8e-5.  That costs nothing where memory is the bound and the clock holds, 2 % of the bf16 cases'
+// times, and 6 % of the long E4M3 case's when it runs for seconds (121 for 113 us): the card is then at its
+// power cap, and the clock gives way to the second product.
 //
 // Bound by HBM once contexts are long; about 8 us go to the launches, to the chain of lengths, pages
 // and keys, and to the join.  On a B200, replayed from a graph: 2 x 131071 keys, 32 query and 4 kv heads,
-// d=128, bf16 93 us (5.8 TB/s), 32 rows of 0 to 4096 keys, 32 and 8 heads 50.7 us (5.3 TB/s), 64 rows of
-// 1024 to 8192 keys, 64 and 8 heads, E4M3 107 us (5.7 TB/s), one row of 300 keys 7.9 us.  (With the
-// queries on the 16-row side, 2 CTAs of 3 stages and a serial join: 105, 56, 137 and 8.0 us.)
+// d=128, bf16 95 us (5.6 TB/s), 32 rows of 0 to 4096 keys, 32 and 8 heads 52 us (5.2 TB/s), 64 rows of
+// 1024 to 8192 keys, 64 and 8 heads, E4M3 107.5 us (5.6 TB/s), one row of 300 keys 8.6 us.  More than 8
+// query heads per kv head take a second column of products (32 rows of 4096 keys, 32 and 2 heads, d=128,
+// bf16 40 us, 3.4 TB/s: the products and P's terms then count), more than 16 a second reading of K and V
+// (4 x 32768 keys, 32 heads and 1 36.6 us, twice 1.8 TB/s, from L2 in part).
 constexpr int kWarps = 4;
 constexpr int kMaxCtasPerSm = 3;
 constexpr int kMaxRows = 16;
